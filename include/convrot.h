@@ -333,6 +333,140 @@ CONVROT_API int convrot_w4a4_linear_noalloc(const void* x, int32_t x_dtype, int6
                                             int64_t g, const uint8_t* wq, const float* ws,
                                             int64_t N, const void* bias, void* y, void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Decoding operators: what stands between the layers of a transformer that generates token by
+ * token with rotated, quantized weights and a rotated, quantized cache.  The conventions above
+ * hold (device pointers of the caller, checks on the host first, kernel launches only).
+ *
+ * Four-bit weights with group scales, activations not quantized (for few rows the weights are
+ * the traffic and quantizing x would save nothing):
+ *   K' = K rounded up to a multiple of max(g, sg); g in {0, 16, 64, 256, 1024}, 0 meaning no
+ *   rotation; sg in {32, 64, 128}: every sg consecutive (rotated) values of a row share a bf16
+ *   scale, s = bf16_rne(fp32(max |value| / 7)), code = clamp(rne(fp32(value / s)), -8, 7), codes
+ *   0 where s = 0; packing as for int4 above.
+ *   y[m][n] = bf16( sum_j s[n][j] sum_{k in group j} code[n][k] xr[m][k] + bias[n] ),
+ *   xr = x zero-padded to K' and rotated in windows of g, rounded to fp16 after an exact
+ *   power-of-two scaling of every 256 values (relative 2^-12); all sums fp32.
+ *   A weight group that holds an Inf or a NaN (or overflows in the rotation) gets a NaN scale;
+ *   an activation row that holds one gives a NaN output row.
+ * --------------------------------------------------------------------------------------- */
+
+/* K' of the group-scaled layer, or a negative status (GROUP, UNSUPPORTED, SHAPE). */
+CONVROT_API int64_t convrot_w4a16_padded_k(int64_t K, int64_t g, int64_t sg);
+
+/* Offline weight path: w [N][K] (row stride K) -> wq uint8 [N][K'/2] (16-byte aligned), ws bf16
+ * [N][K'/sg] (2-byte aligned).  N = 0 is a no-op.  K' <= CONVROT_MAX_KP.
+ * Errors: GROUP, UNSUPPORTED, SHAPE, NULL, DTYPE, ALIGN, HIP. */
+CONVROT_API int convrot_quant_weight_g4(const void* w, int32_t w_dtype, int64_t N, int64_t K, int64_t g,
+                                        int64_t sg, uint8_t* wq, void* ws, void* stream);
+
+/* Bytes of device workspace convrot_w4a16_linear needs (0 for one or two rows, which take a
+ * single launch); 0 as well for arguments it would refuse. */
+CONVROT_API size_t convrot_w4a16_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t g, int64_t sg);
+
+/* The layer: x [M][ldx], ldx >= K (any alignment of the element type), y bf16 [M][N] (2-byte
+ * aligned), bias bf16 [N] or NULL.  Made for M up to some 64 rows; more run too, 64 at a time
+ * (M <= 4194240).  workspace 256-byte aligned, NULL where it needs 0 bytes.  M = 0 or N = 0 is a
+ * no-op.  Results do not depend on the run; rows do not depend on one another.
+ * Errors: GROUP, UNSUPPORTED, SHAPE, NULL, DTYPE, ALIGN, WORKSPACE, HIP. */
+CONVROT_API int convrot_w4a16_linear(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx,
+                                     int64_t g, int64_t sg, const uint8_t* wq, const void* ws, int64_t N,
+                                     const void* bias, void* y, void* workspace, size_t ws_bytes,
+                                     void* stream);
+
+/* Rotary positions.  Frequencies first, on the HOST: out[i], i < R/2 (R even, 2 to 1024), from
+ * f_i = base^(-2i/R), computed in fp64 and rounded once:
+ *   CONVROT_ROPE_PLAIN    f_i
+ *   CONVROT_ROPE_LINEAR   f_i / factor (positions interpolated)
+ *   CONVROT_ROPE_NTK      base scaled by factor^(R/(R-2)): the last frequency is divided by
+ *                         factor, the first stays (R > 2)
+ *   CONVROT_ROPE_BANDS    f_i (w + (1 - w) / factor), w = clamp((turns - low) / (high - low), 0, 1),
+ *                         turns = original * f_i / (2 pi): bands that turn at least `high` times over
+ *                         the original context stay, those below `low` turns are interpolated
+ * factor >= 1 (ignored by PLAIN); original > 0 and 0 <= low < high for BANDS.
+ * Errors: SHAPE (R), UNSUPPORTED (scaling, base <= 0, factor, bands), NULL. */
+enum { CONVROT_ROPE_PLAIN = 0, CONVROT_ROPE_LINEAR = 1, CONVROT_ROPE_NTK = 2, CONVROT_ROPE_BANDS = 3 };
+CONVROT_API int convrot_rotary_frequencies(int64_t R, double base, int32_t scaling, double factor,
+                                           double original, double low, double high, float* out);
+
+/* q [T][Hq][D] and k [T][Hk][D] turned by the positions of their tokens, angle = pos[t] *
+ * inv_freq[i] (taken in fp64, so far positions keep their accuracy; |pos| < 2^53):
+ *   a' = factor (a cos - b sin), b' = factor (b cos + a sin)
+ * on the pairs (2i, 2i+1) (interleaved != 0) or (i, i + R/2) of the first R elements of each head;
+ * the others are copied.  inverse != 0 turns by -angle: the transpose, so the gradient of the
+ * outputs becomes that of the inputs (factor is applied as well), and keys can be moved.
+ * Strides are in elements, of tokens (_t) and heads (_h); elements of a head are contiguous.
+ * Outputs may be the inputs themselves (the same pointer and strides), but not overlap them
+ * otherwise.  Hk = 0 or Hq = 0: no such tensor (its pointers may be NULL).  dtype of all four.
+ * inv_freq fp32 [R/2], pos int64 [T].  T = 0 is a no-op.  R even, 2 <= R <= D <= 1024; at most 65535
+ * heads.  Errors: DTYPE, SHAPE, UNSUPPORTED, NULL, ALIGN, HIP. */
+CONVROT_API int convrot_rotary(const void* q, int64_t q_t, int64_t q_h, void* q_out, int64_t qo_t, int64_t qo_h,
+                               int64_t Hq, const void* k, int64_t k_t, int64_t k_h, void* k_out, int64_t ko_t,
+                               int64_t ko_h, int64_t Hk, int32_t dtype, int64_t T, int64_t D, int64_t R,
+                               const int64_t* pos, const float* inv_freq, int32_t interleaved, float factor,
+                               int32_t inverse, void* stream);
+
+/* The paged 8-bit key/value cache.  A page holds `page` (16, 32, 64 or 128) tokens of one sequence:
+ *   kc int8 [num_pages][H][page][D], ks fp32 [num_pages][H]: key = code * scale, rotated in windows
+ *   of g (0: not; else 16, 64 or 256, a divisor of D) by H_g / sqrt(g);
+ *   vc int8 [num_pages][H][D][page], vs fp32 [num_pages][H]: value = code * scale (not rotated).
+ * D a multiple of 16, at most 256.  kc, vc 16-byte aligned.
+ *
+ * A batch is described on the DEVICE, by the same three int32 arrays for every call of a step:
+ *   cu [B+1]      the rows of sequence b among the call's T rows are cu[b] ... cu[b+1]-1;
+ *   lens [B]      its length, those rows included: they are its last tokens;
+ *   table [B][max_pages] (row stride table_ld): its pages in order.
+ * What does not fit is skipped, never followed: sequences whose rows are not within [0, T], table
+ * entries outside [0, num_pages), tokens beyond max_pages pages.  max_new and max_len are the largest
+ * row count and length the caller expects; they only size the launch, and larger ones are right
+ * too.  A page that receives rows must belong to one sequence; pages that are only read may be
+ * shared. */
+
+/* Writes rows k, v [T][H][D] (strides in elements) into the cache.  The scale of a page covers its
+ * tokens: S = fp32(max |value| / 127) of the new rows, or the page's scale if tokens of this sequence
+ * are in the page already and it is larger; those tokens' codes become rne(code * fp32(S_old / S)).
+ * New codes: clamp(rne(fp32(value / S)), -127, 127).  S below 2^-80 is stored as 0, with codes 0; a page
+ * that receives an Inf or a NaN gets a NaN scale.  Slots behind the last token are left as they were.
+ * T = 0 or B = 0 is a no-op.  Errors: GROUP, UNSUPPORTED, SHAPE, NULL, DTYPE, ALIGN, HIP. */
+CONVROT_API int convrot_kv8_append(const void* k, int64_t k_t, int64_t k_h, const void* v, int64_t v_t,
+                                   int64_t v_h, int32_t dtype, int64_t T, const int32_t* cu,
+                                   const int32_t* lens, const int32_t* table, int64_t table_ld, int64_t B,
+                                   int64_t max_pages, int8_t* kc, float* ks, int8_t* vc, float* vs,
+                                   int64_t num_pages, int64_t page, int64_t H, int64_t D, int64_t g,
+                                   int64_t max_new, void* stream);
+
+/* Reads the rows back, bf16 k, v [T][H][D] contiguous (16-byte aligned), keys rotated back: with cu
+ * the running sum of lens, the whole sequences.  Rows without a page come out as zeros; rows of no
+ * sequence are left as they were.  Errors as for append. */
+CONVROT_API int convrot_kv8_read(const int32_t* cu, const int32_t* lens, const int32_t* table,
+                                 int64_t table_ld, int64_t B, int64_t max_pages, const int8_t* kc,
+                                 const float* ks, const int8_t* vc, const float* vs, int64_t num_pages,
+                                 int64_t page, int64_t H, int64_t D, int64_t g, int64_t max_new, int64_t T,
+                                 void* k, void* v, void* stream);
+
+/* Bytes of device workspace convrot_kv8_attention needs; 0 where it needs none or would refuse. */
+CONVROT_API size_t convrot_kv8_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D,
+                                                         int64_t max_new, int64_t max_len);
+
+/* Attention of the rows q [T][Hq][D] (strides in elements) over the cache, rows of the batch as above
+ * with their keys and values appended: row i of sequence b stands at position lens[b] - n + i and sees
+ * the tokens up to it.  Query head hq reads cached head hq / (Hq / H).
+ *   out[t][hq] = bf16( sum_j p_j v_j ), p = softmax_j(scale q.k_j); out contiguous, 16-byte aligned.
+ * Scores, statistics and sums are fp32; q (rotated by g as the keys were) and the weights p times the
+ * page's value scale enter the products rounded to fp16 (2^-12 relative).  A row that sees no token
+ * is zero; rows of no sequence are left as they were; a row whose q holds an Inf or a NaN, or that sees a
+ * page with a NaN scale, is NaN.  Scales are 0 or at least 2^-80, as append writes them.
+ * Results do not depend on the run.  workspace 256-byte aligned, NULL where it needs 0 bytes; T, B, Hq, H,
+ * D, max_new and max_len as given to the workspace function.
+ * Errors: GROUP, UNSUPPORTED, SHAPE, NULL, DTYPE, ALIGN, WORKSPACE, HIP. */
+CONVROT_API int convrot_kv8_attention(const void* q, int64_t q_t, int64_t q_h, int32_t dtype, int64_t T,
+                                      int64_t Hq, const int32_t* cu, const int32_t* lens,
+                                      const int32_t* table, int64_t table_ld, int64_t B, int64_t max_pages,
+                                      const int8_t* kc, const float* ks, const int8_t* vc, const float* vs,
+                                      int64_t num_pages, int64_t page, int64_t H, int64_t D, int64_t g,
+                                      float scale, int64_t max_new, int64_t max_len, void* out,
+                                      void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

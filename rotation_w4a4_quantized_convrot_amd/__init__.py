@@ -16,6 +16,12 @@ from ._lib import (  # noqa: F401
     convrot_quant_rows_int4, convrot_dequant_int4,
 )
 from .linear import ConvLinear4bit, ConvLinear8bit, ConvLinearFP4  # noqa: F401
+from .decode import (  # noqa: F401
+    ConvAttention, ConvLinearW4A16, KVCache8bit, convrot_kv8_append, convrot_kv8_attention,
+    convrot_kv8_attention_workspace_bytes, convrot_kv8_read, convrot_quant_weight_g4, convrot_rotary,
+    convrot_rotary_frequencies, convrot_w4a16_linear, convrot_w4a16_padded_k,
+    convrot_w4a16_workspace_bytes,
+)
 
 __all__ = [
     "ConvLinear4bit", "ConvLinear8bit", "ConvLinearFP4", "ConvRotError", "load_library", "convrot_status_string", "convrot_version",
@@ -26,4 +32,8 @@ __all__ = [
     "convrot_rotate_quant_act_mxfp4", "convrot_quant_weight_mxfp4", "convrot_mxfp4_gemm",
     "convrot_mxfp4_workspace_bytes", "convrot_mxfp4_linear", "convrot_w4a4_linear_noalloc",
     "convrot_w4a4_linear_fused", "convrot_quant_rows_int4", "convrot_dequant_int4",
+    "ConvLinearW4A16", "KVCache8bit", "ConvAttention", "convrot_quant_weight_g4",
+    "convrot_w4a16_linear", "convrot_w4a16_padded_k", "convrot_w4a16_workspace_bytes",
+    "convrot_rotary", "convrot_rotary_frequencies", "convrot_kv8_append", "convrot_kv8_read",
+    "convrot_kv8_attention", "convrot_kv8_attention_workspace_bytes",
 ]

@@ -32,6 +32,9 @@ CONVROT_NOALLOC_SCRATCH_BYTES = 72 << 20
 
 # (name, restype, argtypes) of every symbol include/convrot.h declares.
 _c_int, _i32, _i64, _vp = ctypes.c_int, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
+_f64 = ctypes.c_double
+_BATCH = [_vp, _vp, _vp, _i64, _i64, _i64]                  # cu, lens, table, its row stride, B, pages
+_CACHE = [_vp, _vp, _vp, _vp] + [_i64] * 5                  # kc, ks, vc, vs, pages, page, H, D, g
 SIGNATURES = {
     "convrot_status_string": (ctypes.c_char_p, [_c_int]),
     "convrot_version": (_c_int, []),
@@ -64,6 +67,20 @@ SIGNATURES = {
                                            _vp, ctypes.c_size_t, _vp, _vp]),
     "convrot_quant_rows_int4": (_c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _vp]),
     "convrot_dequant_int4": (_c_int, [_vp, _vp, _i64, _i64, _vp, _vp]),
+    "convrot_w4a16_padded_k": (_i64, [_i64, _i64, _i64]),
+    "convrot_quant_weight_g4": (_c_int, [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "convrot_w4a16_workspace_bytes": (ctypes.c_size_t, [_i64] * 5),
+    "convrot_w4a16_linear": (_c_int, [_vp, _i32, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _vp,
+                                      _vp, _vp, ctypes.c_size_t, _vp]),
+    "convrot_rotary_frequencies": (_c_int, [_i64, _f64, _i32, _f64, _f64, _f64, _f64, _vp]),
+    "convrot_rotary": (_c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _i64] * 2
+                       + [_i32, _i64, _i64, _i64, _vp, _vp, _i32, ctypes.c_float, _i32, _vp]),
+    "convrot_kv8_append": (_c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _i32, _i64] + _BATCH + _CACHE
+                           + [_i64, _vp]),
+    "convrot_kv8_read": (_c_int, _BATCH + _CACHE + [_i64, _i64, _vp, _vp, _vp]),
+    "convrot_kv8_attention_workspace_bytes": (ctypes.c_size_t, [_i64] * 7),
+    "convrot_kv8_attention": (_c_int, [_vp, _i64, _i64, _i32, _i64, _i64] + _BATCH + _CACHE
+                              + [ctypes.c_float, _i64, _i64, _vp, _vp, ctypes.c_size_t, _vp]),
 }
 
 _lib: Optional[ctypes.CDLL] = None

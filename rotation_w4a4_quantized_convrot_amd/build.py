@@ -14,7 +14,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libconvrot.so")
-SOURCES = ("api.hip", "rht_quant.hip", "w4a4_gemm.hip", "fused.hip", "rowquant.hip")
+SOURCES = ("api.hip", "rht_quant.hip", "w4a4_gemm.hip", "fused.hip", "rowquant.hip",
+           "api_decode.hip", "w4a16.hip", "rotary.hip", "kv8.hip")
 CALIB_PATH = os.path.join(PKG, "libconvrot_calib.so")
 CALIB_SOURCES = ("calib.hip",)
 ARCH = "gfx950"

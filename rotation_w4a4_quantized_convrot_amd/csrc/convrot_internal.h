@@ -69,4 +69,72 @@ hipError_t launch_quant_rows_int4(const float* y, int64_t M, int64_t K, int64_t 
 hipError_t launch_dequant_int4(const uint8_t* q, const float* s, int64_t M, int64_t K,
                                double* out, hipStream_t stream);
 
+// Offline weights with group scales (w4a16.hip): rotate rows of w [N][K] (padded to Kp) in
+// windows of g (0: no rotation), one bf16 scale per sg values, 4-bit codes.
+hipError_t launch_quant_weight_g4(const void* w, int w_dtype, int64_t N, int64_t K, int g, int sg, int64_t Kp,
+                                  uint8_t* wq, uint16_t* ws, hipStream_t stream);
+
+// How the W4A16 product of M rows runs, and the workspace it needs.
+struct W4A16Plan {
+  int64_t units;        // of 256 columns of the padded depth
+  int parts;            // of K that different workgroups take
+  int64_t rows_padded;  // activation rows of the prepared operand; 0: one launch, no workspace
+  size_t operand_bytes, factor_bytes, partial_bytes;
+};
+W4A16Plan plan_w4a16(int64_t M, int64_t N, int64_t Kp);
+hipError_t launch_w4a16_linear(const void* x, int x_dtype, int64_t M, int64_t K, int64_t ldx, int g, int sg,
+                               int64_t Kp, const uint8_t* wq, const uint16_t* ws, int64_t N,
+                               const uint16_t* bias, uint16_t* y, void* workspace, hipStream_t stream);
+
+// Rotary positions (rotary.hip): strides in elements; heads 0: no such tensor.
+struct RotaryPart {
+  const void* in;
+  void* out;
+  int64_t in_t, in_h, out_t, out_h;
+  int heads;
+};
+struct RotaryArgs {
+  RotaryPart q, k;
+  const int64_t* pos;
+  const float* inv_freq;
+  float factor;
+  int D, R, interleaved, inverse;
+};
+hipError_t launch_rotary(const RotaryArgs& a, int dtype, int64_t T, hipStream_t stream);
+
+// The paged 8-bit key/value cache (kv8.hip).
+struct Kv8Batch {
+  const int32_t* cu;     // [B + 1]: first row of each sequence among the T rows
+  const int32_t* lens;   // [B]: tokens of each sequence, the rows' own included
+  const int32_t* table;  // [B][table_ld]: pages of each sequence
+  int64_t B, T, table_ld, max_pages;
+};
+struct Kv8Cache {
+  int8_t* kc;   // [num_pages][H][page][D]
+  float* ks;    // [num_pages][H]
+  int8_t* vc;   // [num_pages][H][D][page]
+  float* vs;    // [num_pages][H]
+  int64_t num_pages;
+  int page, H, D;
+};
+hipError_t launch_kv8_append(const void* k, const void* v, int dtype, int64_t k_t, int64_t k_h, int64_t v_t,
+                             int64_t v_h, const Kv8Batch& b, const Kv8Cache& c, int g, int64_t max_new,
+                             hipStream_t stream);
+hipError_t launch_kv8_read(const Kv8Batch& b, const Kv8Cache& c, int g, int64_t max_new, uint16_t* k,
+                           uint16_t* v, hipStream_t stream);
+
+// Attention over it: how the work is split, and the workspace that needs.
+struct Kv8Plan {
+  int row_tiles;       // 16-row tiles of a workgroup (share) or of each of its waves
+  bool share;          // a workgroup's waves share its rows and split the tokens
+  int64_t row_blocks;  // per sequence and cached head
+  int splits;          // of a sequence's tokens
+  size_t bytes;
+};
+Kv8Plan plan_kv8_attention(int64_t B, int64_t T, int64_t Hq, int64_t H, int64_t D, int64_t max_new,
+                           int64_t max_len);
+hipError_t launch_kv8_attention(const void* q, int dtype, int64_t q_t, int64_t q_h, int64_t Hq,
+                                const Kv8Batch& b, const Kv8Cache& c, int g, float scale, const Kv8Plan& p,
+                                uint16_t* out, void* workspace, hipStream_t stream);
+
 }  // namespace convrot
