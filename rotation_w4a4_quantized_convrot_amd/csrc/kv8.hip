@@ -10,6 +10,7 @@
 #include "decode_device.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace convrot {
 namespace {
@@ -241,8 +242,10 @@ __global__ __launch_bounds__(kThreads) void read_kernel(Kv8Batch batch, Kv8Cache
 }
 
 // ------------------------------------------------------------------------------- attention
-constexpr float kNothing = -1e30f;   // running maximum before the first token
+constexpr float kNothing = -1e30f;   // reference of a row before its first token
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kShift = 7.0f;       // weights are kept times 2^kShift ...
+constexpr float kSlack = 8.0f;       // ... and may pass their reference by 2^kSlack: 2^15 fits fp16
 
 // Eight int8 codes to fp16, exactly: 0x6400 + (code + 128) is the fp16 1024 + code + 128.
 __device__ __forceinline__ half8 decode_i8(uint32_t a, uint32_t b) {
@@ -274,6 +277,11 @@ __device__ __forceinline__ float sum_over_lane_rows(float v) {
   return v + __shfl_xor(v, 32);
 }
 
+// A barrier for what is in LDS: loads from memory may still be on their way.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 struct AttentionArgs {
   const void* q;
   int64_t q_t, q_h;
@@ -283,121 +291,252 @@ struct AttentionArgs {
   int64_t row_blocks, rows;       // rows: T * Hq, of the partial results
   uint16_t* out;
   float* partial;                 // [splits][rows][D], or NULL: one split, straight to out
-  float2* stats;                  // [splits][rows]: running maximum and sum
+  float2* stats;                  // [splits][rows]: reference and sum
 };
 
-// One pass over the tokens with a running maximum.  With s_j = scale q.k_j in powers of two and
-// page scale vs_j, the kept sums are relative to M = max(s_j + log2 vs_j):
-//   w_j = 2^(s_j + log2 vs_j - M + 14),   O = sum w_j vcode_j,   l = sum w_j / vs_j,
-// so that O / l is the answer, the page scale of the values costs nothing in P V, and w_j rounded to
-// fp16 uses that type's range from 2^14 down (a weight 2^-28 of the largest is still normal).
-//
+// What a workgroup works on: a block of the rows of one sequence and cached head, and a share of
+// the sequence's tokens in blocks of 64.
+struct Work {
+  Sequence seq;
+  int64_t b, h, len, before, rows, rb, split;
+};
+
+__device__ __forceinline__ Work work_of(const AttentionArgs& a, const Kv8Batch& batch, const Kv8Cache& cache) {
+  // the cached head varies fastest: with 8 of them each of the chip's 8 L2s sees one head; the
+  // rows that see most come first
+  Work w;
+  int64_t id = blockIdx.x;
+  w.h = id % cache.H;
+  id /= cache.H;
+  w.split = id % a.splits;
+  id /= a.splits;
+  w.rb = a.row_blocks - 1 - id % a.row_blocks;
+  w.b = id / a.row_blocks;
+  w.seq = sequence_of(batch, w.b);
+  w.rows = w.seq.n * (a.Hq / cache.H);
+  w.len = max(min(w.seq.len, batch.max_pages * cache.page), int64_t(0));
+  w.before = w.seq.len - w.seq.n;
+  return w;
+}
+
+// A sequence's pages as a lane sees them.  A look-up is a plain load that nothing waits for or
+// branches on (its column is that of a token below the limit, so it is in the table); what it gave is
+// checked when it is used, a block or two later.
+struct Pages {
+  const int32_t* row;           // of the table
+  const int8_t *k, *v;          // of the cached head, in page 0
+  const float *ks, *vs;
+  uint32_t num_pages, stride, heads, limit, mask;
+  int log;
+
+  __device__ __forceinline__ int32_t find(uint32_t base, uint32_t off) const {
+    return row[min(min(base, limit) + off, limit - 1) >> log];
+  }
+  __device__ __forceinline__ bool there(int32_t id, uint32_t base, uint32_t off) const {
+    return uint32_t(id) < num_pages && base < limit && off < limit - base;
+  }
+  __device__ __forceinline__ uint32_t safe(int32_t id) const { return uint32_t(id) < num_pages ? uint32_t(id) : 0u; }
+  __device__ __forceinline__ const int8_t* keys(int32_t id) const { return k + uint64_t(safe(id)) * stride; }
+  __device__ __forceinline__ const int8_t* values(int32_t id) const { return v + uint64_t(safe(id)) * stride; }
+};
+
+__device__ __forceinline__ Pages pages_of(const Kv8Batch& batch, const Kv8Cache& cache, const Work& w, int64_t limit) {
+  const int64_t head = w.h * cache.page * cache.D;
+  return Pages{batch.table + w.b * batch.table_ld, cache.kc + head, cache.vc + head, cache.ks + w.h, cache.vs + w.h,
+               uint32_t(cache.num_pages), uint32_t(cache.H) * uint32_t(cache.page * cache.D), uint32_t(cache.H),
+               uint32_t(limit), uint32_t(cache.page - 1), 31 - __clz(cache.page)};
+}
+
+// Sixteen values of query row r of a (sequence, cached head), rotated and scaled into fp16's range, to
+// 16 places of LDS; `factor` takes the row's score scale, in powers of two.  A row of 16 lanes
+// holds the row.  A negative scale's sign goes to the query, so that score scales are never
+// negative.
+template <typename TIn, int DT>
+__device__ __forceinline__ void stage_query(const AttentionArgs& a, const Kv8Cache& cache, const Work& w, int64_t r,
+                                            int n, _Float16* row, float* factor) {
+  const int G = a.Hq / cache.H;
+  const bool there = r < w.rows && n * 16 < cache.D;
+  const int64_t t = w.seq.row0 + (there ? r / G : 0), hq = w.h * G + (there ? r % G : 0);
+  const TIn* p = static_cast<const TIn*>(a.q) + (there ? t * a.q_t + hq * a.q_h + n * 16 : 0);
+  float v[16];
+  load16<TIn>(p, there ? 16 : 0, a.q_wide, v);
+  float up, back;
+  half_range(row_max(abs_max16(v)), a.digits, &up, &back);
+  up = a.scale < 0.0f ? -up : up;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] *= up;
+  rotate16(v, a.digits);
+  if (n * 16 < DT) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      half8 o;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = (_Float16)v[8 * k + e];
+      *reinterpret_cast<half8*>(&row[n * 16 + 8 * k]) = o;
+    }
+  }
+  if (n == 0) *factor = back * fabsf(a.scale) * kLog2e;
+}
+
+// The page scales of the 16 tokens whose scores a lane holds.
+struct PageScale {
+  float ks, vs;
+  bool there;
+};
+
+// A token's place from the share's first one; what is far beyond it all the same.
+__device__ __forceinline__ int from_here(int64_t token, int64_t first) {
+  return int(max(min(token - first, int64_t(1) << 30), int64_t(-1)));
+}
+
+__device__ __forceinline__ PageScale scale_of(const Pages& p, int32_t id, uint32_t base, uint32_t off) {
+  const uint64_t at = uint64_t(p.safe(id)) * p.heads;
+  return PageScale{p.ks[at], p.vs[at], p.there(id, base, off)};
+}
+
+// A block of 64 scores a row (16 of them in each lane) to weights, with the running reference m, sum l
+// and output o of each row.  With s_j = scale q.k_j in powers of two, vs_j the page's value scale and
+// R the reference, at most kSlack below max(s_j + log2 vs_j):
+//   w_j = 2^(s_j + log2 vs_j - R + kShift),   o = sum w_j vcode_j,   l = sum w_j / vs_j,
+// so o / l is the answer, the page scale of the values costs nothing in the second product, and w_j
+// rounded to fp16 (2^-12 relative; below 2^-21 of the reference an absolute 2^-32 of it) uses that
+// type's range.  The reference moves only when a score passes it by 2^kSlack, so that o is rarely
+// scaled again.
+// `ragged`: some token of the block is not there or not seen by some row; token (the lane's first),
+// limit and sees (a row's last token) count from the share's first token.
+template <int RT, int TILES>
+__device__ __forceinline__ void weigh(float4_t (&s)[4][RT], const PageScale& page, bool ragged, int token,
+                                      int limit, const float (&row_scale)[RT], const int (&sees)[RT],
+                                      float (&m)[RT], float (&l)[RT], float4_t (&o)[TILES][RT], half8 (&w0)[RT],
+                                      half8 (&w1)[RT]) {
+  const float lv = page.vs == 0.0f ? 0.0f : __builtin_amdgcn_logf(page.vs);
+  const float over_vs = __builtin_amdgcn_exp2f(-lv);
+  const bool no_values = __any(page.vs == 0.0f);
+  float mul[RT], high[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    mul[rt] = row_scale[rt] * page.ks;
+    if (ragged) {
+      const int seen = page.there ? min(sees[rt], limit - 1) - token : -1;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (4 * t + i > seen) s[t][rt][i] = -INFINITY;
+    }
+    float top = s[0][rt][0];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, s[t][rt][i]);
+    high[rt] = fmaxf(kNothing, max_over_lane_rows(top * mul[rt] + lv));
+  }
+  bool grown = false;
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) grown = grown || high[rt] > m[rt] + kSlack;
+  if (__any(grown)) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const float now = fmaxf(m[rt], high[rt]);
+      const float down = __builtin_amdgcn_exp2f(m[rt] - now);
+      m[rt] = now;
+      l[rt] *= down;
+#pragma unroll
+      for (int dt = 0; dt < TILES; ++dt) o[dt][rt] *= down;
+    }
+  }
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const float add = lv - m[rt] + kShift;
+    float sum = 0.0f;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][rt][i], mul[rt], add));
+        if (ragged && s[t][rt][i] == -INFINITY) w = 0.0f;      // also where mul or add is NaN
+        s[t][rt][i] = w;
+        sum += w;
+      }
+    l[rt] += sum == 0.0f ? 0.0f : sum * over_vs;
+    w0[rt] = pack_half8(s[0][rt], s[1][rt]);
+    w1[rt] = pack_half8(s[2][rt], s[3][rt]);
+    if (no_values && page.vs == 0.0f) w0[rt] = w1[rt] = half8{};
+  }
+}
+
+__device__ __forceinline__ uint2_t pack_bf16x4(const float4_t& v, float mul) {
+  uint2_t w;
+  w[0] = uint32_t(f32_to_bf16(v[0] * mul)) | (uint32_t(f32_to_bf16(v[1] * mul)) << 16);
+  w[1] = uint32_t(f32_to_bf16(v[2] * mul)) | (uint32_t(f32_to_bf16(v[3] * mul)) << 16);
+  return w;
+}
+
+// Four values of a row's answer, or of its share of the sums.
+__device__ __forceinline__ void put(const AttentionArgs& a, int D, int64_t split, int64_t row, int d,
+                                    const float4_t& v, float over_l) {
+  if (a.partial != nullptr) *reinterpret_cast<float4_t*>(a.partial + (split * a.rows + row) * D + d) = v;
+  else *reinterpret_cast<uint2_t*>(a.out + row * D + d) = pack_bf16x4(v, over_l);
+}
+
 // Both products run on v_mfma_f32_16x16x32_f16 with the codes exact in fp16.  Scores are computed
-// transposed, tokens x rows: a lane then holds one row's 16 tokens of the 16 that follow one
+// transposed, tokens x rows: a lane then holds one row's scores of 16 tokens that follow one
 // another (lane row c: tokens 16 c ... of a block of 64), which is the layout the second product's
 // operand needs, so the weights never leave the registers; the row statistics need two lane
 // exchanges a block.  Rows are (query, head of the group) pairs of one cached head.
-//
-// SHARE (few rows): the four waves of a workgroup take every fourth block of tokens of the same
-// RT * 16 rows and add up through LDS at the end.  Else each wave has RT * 16 rows of its own.
-template <typename TIn, int DT, int RT, bool SHARE>
-__global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Kv8Batch batch, Kv8Cache cache) {
+
+// Few rows (up to 16 * RT of a cached head): the four waves of a workgroup take every fourth block of
+// tokens, straight from memory into their registers, and add up through LDS at the end.  The cache's
+// bytes are the bound: a block's keys are asked for as soon as the last block's are used, its values as
+// soon as those are.
+template <int DT, int RT>
+constexpr size_t few_rows_lds_bytes() {
+  return size_t(4) * 16 * RT * (DT + 4) * 4;
+}
+
+template <typename TIn, int DT, int RT>
+__global__ __launch_bounds__(256, DT * RT <= 128 ? 2 : 1) void few_rows_kernel(AttentionArgs a, Kv8Batch batch, Kv8Cache cache) {
   constexpr int kRows = RT * 16, kQStride = DT + 8, kPieces = DT / 64, kTilesD = DT / 16;
   constexpr int kOStride = DT + 4;
-  constexpr int kQBytes = (SHARE ? 1 : 4) * kRows * kQStride * 2;
-  constexpr int kOBytes = SHARE ? kRows * kOStride * 4 : 0;
-  __shared__ __align__(16) uint8_t lds[kQBytes > kOBytes ? kQBytes : kOBytes];
-  __shared__ float row_factor[(SHARE ? 1 : 4) * kRows];
-  __shared__ float wave_m[SHARE ? 4 : 1][kRows], wave_l[SHARE ? 4 : 1][kRows];
+  extern __shared__ __align__(16) uint8_t lds[];     // few_rows_lds_bytes: the queries, later the sums
+  __shared__ float factor[kRows];
+  __shared__ float wave_m[4][kRows], wave_l[4][kRows];
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, c = lane >> 4;
-  // the cached head varies fastest: with 8 of them each of the chip's 8 L2s sees one head
-  int64_t id = blockIdx.x;
-  const int64_t h = id % cache.H;
-  id /= cache.H;
-  const int split = int(id % a.splits);
-  id /= a.splits;
-  const int64_t rb_first = a.row_blocks - 1 - id % a.row_blocks, b = id / a.row_blocks;
-  const Sequence seq = sequence_of(batch, b);
+  const Work w = work_of(a, batch, cache);
   const int G = a.Hq / cache.H;
-  const int64_t rows = seq.n * G;
-  const int64_t len = max(min(seq.len, batch.max_pages * cache.page), int64_t(0));
-  const int64_t before = seq.len - seq.n;
-  const int page_log = 31 - __clz(cache.page);
-  const int64_t page_bytes = int64_t(cache.page) * cache.D;
+  _Float16* const q_lds = reinterpret_cast<_Float16*>(lds);
 
-  _Float16* const q_lds = reinterpret_cast<_Float16*>(lds) + (SHARE ? 0 : wave * kRows * kQStride);
-  float* const factor = row_factor + (SHARE ? 0 : wave * kRows);
-
-  for (int64_t rb = rb_first; rb * (SHARE ? kRows : 4 * kRows) < rows; rb += a.row_blocks) {
-    const int64_t r0 = SHARE ? rb * kRows : (rb * 4 + wave) * kRows;
-    if constexpr (SHARE) __syncthreads();
-    // the queries: rotated, scaled into fp16's range, to LDS
-    for (int i = (SHARE ? wave * 4 : 0) + c; i < kRows; i += SHARE ? 16 : 4) {
-      const int64_t r = r0 + i;
-      const bool there = r < rows && n * 16 < cache.D;
-      const int64_t t = seq.row0 + (there ? r / G : 0), hq = h * G + (there ? r % G : 0);
-      const TIn* p = static_cast<const TIn*>(a.q) + (there ? t * a.q_t + hq * a.q_h + n * 16 : 0);
-      float v[16];
-      load16<TIn>(p, there ? 16 : 0, a.q_wide, v);
-      float up, back;
-      half_range(row_max(abs_max16(v)), a.digits, &up, &back);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] *= up;
-      rotate16(v, a.digits);
-      if (n * 16 < DT) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          half8 o;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = (_Float16)v[8 * k + e];
-          *reinterpret_cast<half8*>(&q_lds[i * kQStride + n * 16 + 8 * k]) = o;
-        }
-      }
-      if (n == 0) factor[i] = back * a.scale * kLog2e;
-    }
-    if constexpr (SHARE) __syncthreads();
-    else __builtin_amdgcn_wave_barrier();
-
-    half8 q[RT == 1 ? kPieces : 1][2];
-    if constexpr (RT == 1) {
-#pragma unroll
-      for (int p = 0; p < kPieces; ++p)
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          q[p][k] = *reinterpret_cast<const half8*>(&q_lds[n * kQStride + 64 * p + 16 * c + 8 * k]);
-    }
-    float row_scale[RT], m[RT], l[RT];
-    int64_t sees[RT];               // last token that the lane's row may see
-    float4_t o[kTilesD][RT] = {};
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int64_t r = r0 + rt * 16 + n;
-      row_scale[rt] = factor[rt * 16 + n];
-      sees[rt] = r < rows ? before + r / G : int64_t(-1);
-      m[rt] = kNothing;
-      l[rt] = 0.0f;
-    }
+  for (int64_t rb = w.rb; rb * kRows < w.rows; rb += a.row_blocks) {
+    const int64_t r0 = rb * kRows;
     // tokens that any of these rows sees, in blocks of 64; this split's share of them
-    const int64_t r_last = min(r0 + kRows, rows) - 1;
-    const int64_t limit = r0 < rows ? min(len, before + r_last / G + 1) : int64_t(0);
-    const int64_t all_see = r0 < rows ? before + r0 / G : int64_t(-1);   // every row sees tokens up to it
+    const int64_t limit = min(w.len, w.before + (min(r0 + kRows, w.rows) - 1) / G + 1);
     const int64_t blocks = limit > 0 ? (limit + 63) / 64 : 0;
-    const int64_t per = (blocks + a.splits - 1) / a.splits;
-    const int64_t from = split * per, to = min(from + per, blocks);
+    const int64_t per = (blocks + a.splits - 1) / a.splits, from = w.split * per;
+    const int count = int(max(min(per, blocks - from), int64_t(0)));
+    // from here on tokens count from the share's first
+    const int rel_limit = from_here(limit, from * 64);
+    const int all_see = from_here(w.before + r0 / G, from * 64);   // every row sees the tokens up to it
 
-    for (int64_t blk = from + (SHARE ? wave : 0); blk < to; blk += SHARE ? 4 : 1) {
-      const int64_t base = blk * 64;
-      // pages: of the 16 tokens whose keys the lane loads (16 (n / 4) ...), and of those whose
-      // values and scores it holds (16 c ...)
-      const int64_t tk = base + 16 * (n >> 2), tv = base + 16 * c;
-      const int64_t idk = tk < limit ? page_of(batch, cache, b, tk >> page_log) : -1;
-      const int64_t idv = tv < limit ? page_of(batch, cache, b, tv >> page_log) : -1;
-      const int64_t hk = max(idk, int64_t(0)) * cache.H + h, hv = max(idv, int64_t(0)) * cache.H + h;
-      const int8_t* const kp = cache.kc + hk * page_bytes + ((tk & (cache.page - 1)) + (n & 3)) * cache.D;
-      const int8_t* const vp = cache.vc + hv * page_bytes + (tv & (cache.page - 1));
-      uint4_t kw[4][kPieces], vw[kTilesD];
+    // tokens of a block that concern the lane: the 16 whose keys it loads (16 (n / 4) ...), and the 16
+    // whose values and scores it holds (16 c ...)
+    const Pages pages = pages_of(batch, cache, w, limit);
+    const uint32_t off_k = 16 * (n >> 2), off_v = 16 * c, base0 = uint32_t(from) * 64 + wave * 64;
+    int32_t idk = -1, idv = -1, idk1 = -1, idv1 = -1;            // of the first block and the next
+    if (wave < count) {
+      idk = pages.find(base0, off_k);
+      idv = pages.find(base0, off_v);
+      idk1 = pages.find(base0 + 256, off_k);
+      idv1 = pages.find(base0 + 256, off_v);
+    }
+    __syncthreads();
+    for (int i = wave * 4 + c; i < kRows; i += 16)
+      stage_query<TIn, DT>(a, cache, w, r0 + i, n, q_lds + i * kQStride, factor + i);
+
+    uint4_t kw[4][kPieces], vw[kTilesD];
+    const auto load_keys = [&](uint32_t base, int32_t id) {
+      const int8_t* const kp = pages.keys(id) + (((base + off_k) & pages.mask) + (n & 3)) * cache.D;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -405,207 +544,427 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Kv8Batc
           const int d = 64 * p + 16 * c;
           kw[t][p] = *reinterpret_cast<const uint4_t*>(kp + 4 * t * cache.D + (d < cache.D ? d : 0));
         }
-      const float ks = cache.ks[hv], vs = cache.vs[hv];     // of the scores the lane holds
+    };
+    const auto load_values = [&](uint32_t base, int32_t id) {
+      const int8_t* const vp = pages.values(id) + ((base + off_v) & pages.mask);
 #pragma unroll
       for (int dt = 0; dt < kTilesD; ++dt) {
         const int d = 16 * dt + n;
         vw[dt] = *reinterpret_cast<const uint4_t*>(vp + (d < cache.D ? d : 0) * cache.page);
       }
+    };
+    PageScale page{};
+    if (wave < count) {
+      load_keys(base0, idk);
+      page = scale_of(pages, idv, base0, off_v);
+      load_values(base0, idv);
+    }
+    idk = idk1;
+    idv = idv1;
+    lds_barrier();                  // the queries are there; the codes may still be on their way
 
+    half8 q[RT][kPieces][2];
+    float row_scale[RT], m[RT], l[RT];
+    int sees[RT];                   // last token that the lane's row may see
+    float4_t o[kTilesD][RT] = {};
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          q[rt][p][k] = *reinterpret_cast<const half8*>(&q_lds[(rt * 16 + n) * kQStride + 64 * p + 16 * c + 8 * k]);
+      const int64_t r = r0 + rt * 16 + n;
+      row_scale[rt] = factor[rt * 16 + n];
+      sees[rt] = r < w.rows ? from_here(w.before + r / G, from * 64) : -1;
+      m[rt] = kNothing;
+      l[rt] = 0.0f;
+    }
+    // one block; `more`: another follows, whose codes are asked for meanwhile.  Every value that a load
+    // brings for it is asked for after its last use here, and the last block has a copy of the code
+    // of its own, so that nothing has to be moved, or waited for, while it is on its way.
+    const auto step = [&](auto tag, int blk) {
+      constexpr bool more = decltype(tag)::value;
+      const int base = blk * 64;
       float4_t s[4][RT];
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) s[t][rt] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int p = 0; p < kPieces; ++p) {
-        half8 qf[RT][2];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if constexpr (RT == 1) qf[rt][k] = q[p][k];
-            else qf[rt][k] = *reinterpret_cast<const half8*>(&q_lds[(rt * 16 + n) * kQStride + 64 * p + 16 * c + 8 * k]);
-          }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const half8 k0 = decode_i8(kw[t][p][0], kw[t][p][1]), k1 = decode_i8(kw[t][p][2], kw[t][p][3]);
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            s[t][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[rt][0], s[t][rt], 0, 0, 0);
-            s[t][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[rt][1], s[t][rt], 0, 0, 0);
-          }
-        }
-      }
-
-      const float lv = vs == 0.0f ? 0.0f : __builtin_amdgcn_logf(vs);
-      const float over_vs = __builtin_amdgcn_exp2f(-lv);
-      const bool ragged = base + 63 > all_see || base + 64 > limit || __any(idv < 0);
-      const bool no_values = __any(vs == 0.0f);
-      half8 w0[RT], w1[RT];
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const float mul = row_scale[rt] * ks;
-        float top = -INFINITY;
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float x = s[t][rt][i] * mul;
-            if (ragged && (tv + 4 * t + i > sees[rt] || tv + 4 * t + i >= limit || idv < 0)) x = -INFINITY;
-            s[t][rt][i] = x;
-            top = fmaxf(top, x);
-          }
-        const float m_new = fmaxf(m[rt], max_over_lane_rows(top + lv));
-        if (__any(m_new > m[rt])) {
-          const float down = __builtin_amdgcn_exp2f(m[rt] - m_new);
-          l[rt] *= down;
-#pragma unroll
-          for (int dt = 0; dt < kTilesD; ++dt) o[dt][rt] *= down;
-          m[rt] = m_new;
-        }
-        const float add = lv - m[rt] + 14.0f;
-        float sum = 0.0f;
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float w = __builtin_amdgcn_exp2f(s[t][rt][i] + add);
-            if (ragged && s[t][rt][i] == -INFINITY) w = 0.0f;      // also where `add` is NaN
-            s[t][rt][i] = w;
-            sum += w;
-          }
-        l[rt] += sum == 0.0f ? 0.0f : sum * over_vs;
-        w0[rt] = pack_half8(s[0][rt], s[1][rt]);
-        w1[rt] = pack_half8(s[2][rt], s[3][rt]);
-        if (no_values && vs == 0.0f) w0[rt] = w1[rt] = half8{};
-      }
-#pragma unroll
-      for (int dt = 0; dt < kTilesD; ++dt) {
-        const half8 v0 = decode_i8(vw[dt][0], vw[dt][1]), v1 = decode_i8(vw[dt][2], vw[dt][3]);
-#pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-          o[dt][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, w0[rt], o[dt][rt], 0, 0, 0);
-          o[dt][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, w1[rt], o[dt][rt], 0, 0, 0);
+          s[t][rt] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
         }
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const half8 key = decode_i8(kw[t][p][2 * k], kw[t][p][2 * k + 1]);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+              s[t][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q[rt][p][k], s[t][rt], 0, 0, 0);
+          }
+      const uint32_t ahead = uint32_t(from + blk + 4) * 64;
+      if constexpr (more) {
+        load_keys(ahead, idk);
+        idk = pages.find(ahead + 256, off_k);
       }
-    }
+      __builtin_amdgcn_sched_barrier(0);
+      const bool ragged = base + 63 > all_see || base + 64 > rel_limit || __any(!page.there);
+      half8 w0[RT], w1[RT];
+      weigh(s, page, ragged, base + 16 * c, rel_limit, row_scale, sees, m, l, o, w0, w1);
+      if constexpr (more) page = scale_of(pages, idv, ahead, off_v);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int dt = 0; dt < kTilesD; ++dt) {
+          const half8 v = decode_i8(vw[dt][2 * k], vw[dt][2 * k + 1]);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+            o[dt][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, k == 0 ? w0[rt] : w1[rt], o[dt][rt], 0, 0, 0);
+        }
+      if constexpr (more) {
+        load_values(ahead, idv);
+        idv = pages.find(ahead + 256, off_v);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    int blk = wave;
+    for (; blk + 4 < count; blk += 4) step(std::true_type{}, blk);
+    if (blk < count) step(std::false_type{}, blk);
 
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) l[rt] = sum_over_lane_rows(l[rt]);
-
-    if constexpr (SHARE) {
-      // the four waves' sums, added in wave order
-      if (c == 0) {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          wave_m[wave][rt * 16 + n] = m[rt];
-          wave_l[wave][rt * 16 + n] = l[rt];
-        }
-      }
-      __syncthreads();
-      float* const sums = reinterpret_cast<float*>(lds);
-      for (int w = 0; w < 4; ++w) {
-        if (wave == w) {
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            const int r = rt * 16 + n;
-            const float top = fmaxf(fmaxf(wave_m[0][r], wave_m[1][r]), fmaxf(wave_m[2][r], wave_m[3][r]));
-            const float down = __builtin_amdgcn_exp2f(m[rt] - top);
-#pragma unroll
-            for (int dt = 0; dt < kTilesD; ++dt) {
-              float4_t* const at = reinterpret_cast<float4_t*>(&sums[r * kOStride + 16 * dt + 4 * c]);
-              float4_t v = w == 0 ? float4_t{0.0f, 0.0f, 0.0f, 0.0f} : *at;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(o[dt][rt][i], down, v[i]);
-              *at = v;
-            }
-          }
-        }
-        __syncthreads();
-      }
-      // a row of 16 lanes to a row: 16 values a lane
-      for (int i = threadIdx.x >> 4; i < kRows; i += 16) {
-        const int64_t r = r0 + i;
-        const float top = fmaxf(fmaxf(wave_m[0][i], wave_m[1][i]), fmaxf(wave_m[2][i], wave_m[3][i]));
-        float sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) sum += wave_l[w][i] * __builtin_amdgcn_exp2f(wave_m[w][i] - top);
-        if (r >= rows) continue;
-        const int64_t row = (seq.row0 + r / G) * a.Hq + h * G + r % G;
-        if (a.partial != nullptr && n == 0) a.stats[split * a.rows + row] = make_float2(top, sum);
-        for (int d = n * 4; d < cache.D; d += 64) {
-          float4_t v = *reinterpret_cast<const float4_t*>(&sums[i * kOStride + d]);
-          if (a.partial != nullptr) {
-            *reinterpret_cast<float4_t*>(a.partial + (split * a.rows + row) * cache.D + d) = v;
-          } else {
-            const float div = sum == 0.0f ? 0.0f : 1.0f / sum;
-            uint2_t w;
-            w[0] = uint32_t(f32_to_bf16(v[0] * div)) | (uint32_t(f32_to_bf16(v[1] * div)) << 16);
-            w[1] = uint32_t(f32_to_bf16(v[2] * div)) | (uint32_t(f32_to_bf16(v[3] * div)) << 16);
-            *reinterpret_cast<uint2_t*>(a.out + row * cache.D + d) = w;
-          }
-        }
-      }
-    } else {
+    // the four waves' sums, added in wave order
+    if (c == 0) {
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        const int64_t r = r0 + rt * 16 + n;
-        if (r >= rows) continue;
-        const int64_t row = (seq.row0 + r / G) * a.Hq + h * G + r % G;
-        if (a.partial != nullptr && c == 0) a.stats[split * a.rows + row] = make_float2(m[rt], l[rt]);
-        const float div = l[rt] == 0.0f ? 0.0f : 1.0f / l[rt];
-#pragma unroll
-        for (int dt = 0; dt < kTilesD; ++dt) {
-          const int d = 16 * dt + 4 * c;
-          if (d >= cache.D) continue;
-          const float4_t v = o[dt][rt];
-          if (a.partial != nullptr) {
-            *reinterpret_cast<float4_t*>(a.partial + (split * a.rows + row) * cache.D + d) = v;
-          } else {
-            uint2_t w;
-            w[0] = uint32_t(f32_to_bf16(v[0] * div)) | (uint32_t(f32_to_bf16(v[1] * div)) << 16);
-            w[1] = uint32_t(f32_to_bf16(v[2] * div)) | (uint32_t(f32_to_bf16(v[3] * div)) << 16);
-            *reinterpret_cast<uint2_t*>(a.out + row * cache.D + d) = w;
-          }
-        }
+        wave_m[wave][rt * 16 + n] = m[rt];
+        wave_l[wave][rt * 16 + n] = l[rt];
       }
-      __builtin_amdgcn_wave_barrier();   // the wave's queries are read before the next ones come
+    }
+    __syncthreads();                // also: no wave reads the queries any more
+    float* const sums = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int r = rt * 16 + n;
+      const float top = fmaxf(fmaxf(wave_m[0][r], wave_m[1][r]), fmaxf(wave_m[2][r], wave_m[3][r]));
+      const float down = __builtin_amdgcn_exp2f(m[rt] - top);
+#pragma unroll
+      for (int dt = 0; dt < kTilesD; ++dt)
+        *reinterpret_cast<float4_t*>(&sums[(wave * kRows + r) * kOStride + 16 * dt + 4 * c]) = o[dt][rt] * down;
+    }
+    __syncthreads();
+    // a row of 16 lanes to a row
+    for (int i = threadIdx.x >> 4; i < kRows; i += 16) {
+      const int64_t r = r0 + i;
+      if (r >= w.rows) continue;
+      const float top = fmaxf(fmaxf(wave_m[0][i], wave_m[1][i]), fmaxf(wave_m[2][i], wave_m[3][i]));
+      float sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum += wave_l[k][i] * __builtin_amdgcn_exp2f(wave_m[k][i] - top);
+      const int64_t row = (w.seq.row0 + r / G) * a.Hq + w.h * G + r % G;
+      if (a.partial != nullptr && n == 0) a.stats[w.split * a.rows + row] = make_float2(top, sum);
+      const float over_l = sum == 0.0f ? 0.0f : 1.0f / sum;
+      for (int d = n * 4; d < cache.D; d += 64) {
+        float4_t v = *reinterpret_cast<const float4_t*>(&sums[i * kOStride + d]);
+#pragma unroll
+        for (int k = 1; k < 4; ++k) v += *reinterpret_cast<const float4_t*>(&sums[(k * kRows + i) * kOStride + d]);
+        put(a, cache.D, w.split, row, d, v, over_l);
+      }
     }
   }
 }
 
-// Joins the splits of a row in their order: a wave to a row.
+// Operand reads from LDS stay kAhead blocks ahead of the matrix instructions that use them (left
+// alone, the compiler reads each one right before its use and waits for it).
+constexpr int kAhead = 6;
+
+template <int READS, int PER>
+__device__ __forceinline__ void keep_reads_ahead() {
+  __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);       // LDS reads
+#pragma unroll
+  for (int j = kAhead; j < READS; ++j) {
+    __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);        // matrix instructions
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, PER * kAhead, 0);
+}
+
+// Many rows: a workgroup of eight waves takes 8 * 16 * RT rows.  Every block of 64 tokens is decoded
+// once, an eighth by each wave, into the operand layout in LDS (blocks of 1 KB that a wave reads as
+// they are), where all eight waves use it.
+//
+// A block is two phases of a wave, one of vector arithmetic (its weights) and one of matrix
+// instructions (its values' product, then the next block's scores).  The two waves of a SIMD, w and
+// w + 4, are kept one phase apart by a barrier after each, so that the matrix cores work for one
+// while the other has its weights computed.  With phases counted over both groups, waves 0-3 do the
+// weights of block i in phase 2 i and its products in 2 i + 1, waves 4-7 one later: keys of block j
+// are read in phases 2 j - 1 and 2 j, values in 2 j + 1 and 2 j + 2.  In its product phase of block i a
+// wave writes its part of the keys of block i + 2 and of the values of block i + 1: two buffers each
+// are enough, and four places for the page scales (read in phases 2 j and 2 j + 1, written in 2 j - 3).
+template <int DT>
+constexpr size_t many_rows_lds_bytes() {
+  return size_t(DT / 8) * 2048 * 2 + 4 * 64;
+}
+
+template <typename TIn, int DT, int RT>
+__global__ __launch_bounds__(512) void many_rows_kernel(AttentionArgs a, Kv8Batch batch, Kv8Cache cache) {
+  constexpr int kWaveRows = RT * 16, kRows = 8 * kWaveRows;
+  constexpr int kPieces = DT / 64, kTilesD = DT / 16, kQStride = DT + 8;
+  constexpr int kHalf = 4 * kPieces * 2048;            // the keys, or the values, of a block
+  constexpr int kMine = (4 * kPieces + 7) / 8;         // 2 KB jobs of a wave in each half
+  extern __shared__ __align__(16) uint8_t lds[];       // many_rows_lds_bytes
+  uint8_t* const key_lds = lds;
+  uint8_t* const value_lds = lds + 2 * kHalf;
+  float* const scale_lds = reinterpret_cast<float*>(lds + 4 * kHalf);
+  static_assert(4 * kPieces == kTilesD, "as many key tiles as value tiles");
+  static_assert(kWaveRows * kQStride * 2 * 4 <= 4 * kHalf, "the queries of half the waves fit the buffers");
+  __shared__ float factor[kRows];
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, c = lane >> 4;
+  const Work w = work_of(a, batch, cache);
+  const int G = a.Hq / cache.H;
+
+  for (int64_t rb = w.rb; rb * kRows < w.rows; rb += a.row_blocks) {
+    const int64_t r0 = rb * kRows + wave * kWaveRows;
+    half8 q[RT][kPieces][2];
+    float row_scale[RT], m[RT], l[RT];
+    int sees[RT];
+    float4_t o[kTilesD][RT] = {};
+    // the queries go through LDS in the buffers' place, four waves at a time
+    for (int turn = 0; turn < 2; ++turn) {
+      __syncthreads();
+      if ((wave >> 2) == turn) {
+        _Float16* const q_lds = reinterpret_cast<_Float16*>(lds) + (wave & 3) * kWaveRows * kQStride;
+        for (int i = c; i < kWaveRows; i += 4)
+          stage_query<TIn, DT>(a, cache, w, r0 + i, n, q_lds + i * kQStride, factor + wave * kWaveRows + i);
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              q[rt][p][k] = *reinterpret_cast<const half8*>(&q_lds[(rt * 16 + n) * kQStride + 64 * p + 16 * c + 8 * k]);
+      }
+    }
+    __syncthreads();
+    const bool active = r0 < w.rows;                               // the wave has rows
+    // tokens that any row of the workgroup sees, in blocks of 64; this split's share of them
+    const int64_t limit = min(w.len, w.before + (min(rb * kRows + kRows, w.rows) - 1) / G + 1);
+        const int64_t blocks = limit > 0 ? (limit + 63) / 64 : 0;
+    const int64_t per = (blocks + a.splits - 1) / a.splits;
+    const int64_t from = w.split * per;
+    const int count = int(max(min(per, blocks - from), int64_t(0)));
+    // from here on tokens count from the share's first
+    const int rel_limit = from_here(limit, from * 64);
+    const int all_see = from_here(w.before + r0 / G, from * 64);   // every row of the wave sees the tokens up to it
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int64_t r = r0 + rt * 16 + n;
+      row_scale[rt] = factor[wave * kWaveRows + rt * 16 + n];
+      sees[rt] = r < w.rows ? from_here(w.before + r / G, from * 64) : -1;
+      m[rt] = kNothing;
+      l[rt] = 0.0f;
+    }
+
+    const Pages pages = pages_of(batch, cache, w, limit);
+    const uint32_t off_k = 16 * (n >> 2), off_v = 16 * c, base0 = uint32_t(from) * 64;
+    uint4_t raw_k[kMine], raw_v[kMine];
+    PageScale raw_page{};
+    const bool works = kTilesD >= 8 || wave < kTilesD;      // with D <= 64 half the waves have no part
+    const auto load_keys = [&](uint32_t base, int32_t id) {
+      const int8_t* const kp = pages.keys(id) + (((base + off_k) & pages.mask) + (n & 3)) * cache.D;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int job = i * 8 + wave, d = 64 * (job / 4) + 16 * c;
+        if (works) raw_k[i] = *reinterpret_cast<const uint4_t*>(kp + 4 * (job % 4) * cache.D + (d < cache.D ? d : 0));
+      }
+    };
+    const auto load_values = [&](uint32_t base, int32_t id) {
+      const int8_t* const vp = pages.values(id) + ((base + off_v) & pages.mask);
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int d = 16 * (i * 8 + wave) + n;
+        if (works) raw_v[i] = *reinterpret_cast<const uint4_t*>(vp + (d < cache.D ? d : 0) * cache.page);
+      }
+    };
+    const auto write = [&](uint8_t* at, const uint4_t (&raw)[kMine]) {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        if (!works) continue;
+        half8* const p = reinterpret_cast<half8*>(at + (i * 8 + wave) * 2048) + lane;
+        p[0] = decode_i8(raw[i][0], raw[i][1]);
+        p[64] = decode_i8(raw[i][2], raw[i][3]);
+      }
+    };
+    const auto write_scale = [&](int i) {
+      if (wave == 0 && n == 0) {
+        float* const p = scale_lds + (i & 3) * 16 + 4 * c;
+        p[0] = raw_page.ks;
+        p[1] = raw_page.vs;
+        p[2] = raw_page.there ? 1.0f : 0.0f;
+      }
+    };
+    float4_t s[4][RT];
+    const auto scores = [&](int i) {
+      const uint8_t* const at = key_lds + (i & 1) * kHalf;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) s[t][rt] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      const auto fragment = [&](int j) {       // piece j / 8, half j / 4 % 2, token tile j % 4
+        return reinterpret_cast<const half8*>(at + (j / 8 * 4 + j % 4) * 2048)[j / 4 % 2 * 64 + lane];
+      };
+      half8 ring[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) ring[j] = fragment(j);
+#pragma unroll
+      for (int j = 0; j < 8 * kPieces; ++j) {
+        const half8 key = ring[j % kAhead];
+        if (j + kAhead < 8 * kPieces) ring[j % kAhead] = fragment(j + kAhead);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          s[j % 4][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q[rt][j / 8][j / 4 % 2], s[j % 4][rt], 0, 0, 0);
+      }
+      keep_reads_ahead<8 * kPieces, RT>();
+    };
+
+    if (count > 0) {
+      // blocks 0 and 1 of the keys and 0 of the values, then what the first phases write
+      const int32_t k0 = pages.find(base0, off_k), v0 = pages.find(base0, off_v);
+      const int32_t k1 = pages.find(base0 + 64, off_k), v1 = pages.find(base0 + 64, off_v);
+      const int32_t k2 = pages.find(base0 + 128, off_k), v2 = pages.find(base0 + 128, off_v);
+      load_keys(base0, k0);
+      load_values(base0, v0);
+      raw_page = scale_of(pages, v0, base0, off_v);
+      write(key_lds, raw_k);
+      write(value_lds, raw_v);
+      write_scale(0);
+      load_keys(base0 + 64, k1);
+      raw_page = scale_of(pages, v1, base0 + 64, off_v);
+      write(key_lds + kHalf, raw_k);
+      write_scale(1);
+      load_keys(base0 + 128, k2);
+      raw_page = scale_of(pages, v2, base0 + 128, off_v);
+      load_values(base0 + 64, v1);
+      // pages that the product phase of block i needs: for the keys and the scales of block i + 3, for the
+      // values of i + 2.  Past the share's end blocks are loaded from its last token's page and never
+      // used.
+      int32_t idk = pages.find(base0 + 192, off_k), ids = pages.find(base0 + 192, off_v), idv = v2;
+      lds_barrier();
+      if (active) scores(0);
+      if (wave >= 4) lds_barrier();
+      for (int i = 0; i < count; ++i) {
+        half8 w0[RT], w1[RT];
+        if (active) {
+          const float* const ps = scale_lds + (i & 3) * 16 + 4 * c;
+          const PageScale page{ps[0], ps[1], ps[2] != 0.0f};
+          const bool ragged = i * 64 + 63 > all_see || i * 64 + 64 > rel_limit || __any(!page.there);
+          weigh(s, page, ragged, i * 64 + 16 * c, rel_limit, row_scale, sees, m, l, o, w0, w1);
+        }
+        lds_barrier();
+        if (active) {
+          const uint8_t* const at = value_lds + (i & 1) * kHalf;
+          const auto fragment = [&](int j) {   // half j / kTilesD of the tokens, channel tile j % kTilesD
+            return reinterpret_cast<const half8*>(at + j % kTilesD * 2048)[j / kTilesD * 64 + lane];
+          };
+          half8 ring[kAhead];
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) ring[j] = fragment(j);
+#pragma unroll
+          for (int j = 0; j < 2 * kTilesD; ++j) {
+            const half8 v = ring[j % kAhead];
+            if (j + kAhead < 2 * kTilesD) ring[j % kAhead] = fragment(j + kAhead);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+              o[j % kTilesD][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, j < kTilesD ? w0[rt] : w1[rt],
+                                                                         o[j % kTilesD][rt], 0, 0, 0);
+          }
+          keep_reads_ahead<2 * kTilesD, RT>();
+          scores(i + 1);
+        }
+        write(value_lds + ((i + 1) & 1) * kHalf, raw_v);
+        write(key_lds + (i & 1) * kHalf, raw_k);
+        write_scale(i + 2);
+        const uint32_t ahead = uint32_t(from + i) * 64;
+        load_values(ahead + 128, idv);
+        load_keys(ahead + 192, idk);
+        raw_page = scale_of(pages, ids, ahead + 192, off_v);
+        idv = pages.find(ahead + 192, off_v);
+        idk = pages.find(ahead + 256, off_k);
+        ids = pages.find(ahead + 256, off_v);
+        lds_barrier();
+      }
+      if (wave < 4) lds_barrier();
+    }
+
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      l[rt] = sum_over_lane_rows(l[rt]);
+      const int64_t r = r0 + rt * 16 + n;
+      if (r >= w.rows) continue;
+      const int64_t row = (w.seq.row0 + r / G) * a.Hq + w.h * G + r % G;
+      if (a.partial != nullptr && c == 0) a.stats[w.split * a.rows + row] = make_float2(m[rt], l[rt]);
+      const float over_l = l[rt] == 0.0f ? 0.0f : 1.0f / l[rt];
+#pragma unroll
+      for (int dt = 0; dt < kTilesD; ++dt) {
+        const int d = 16 * dt + 4 * c;
+        if (d < cache.D) put(a, cache.D, w.split, row, d, o[dt][rt], over_l);
+      }
+    }
+  }
+}
+
+// Joins the splits of a row: 64 / LANES of them at a time in a wave, LANES lanes to a row's values (4
+// each, several times over), WAVES waves to a row; always in the same order.
+template <int WAVES>
 __global__ __launch_bounds__(256) void join_splits_kernel(Kv8Batch batch, int Hq, int D, int splits, int64_t rows,
                                                           const float* __restrict__ partial,
                                                           const float2* __restrict__ stats,
                                                           uint16_t* __restrict__ out) {
-  const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  constexpr int kPerBlock = 4 / WAVES;
+  __shared__ __align__(16) float4_t part[WAVES == 1 ? 1 : 4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t row = int64_t(blockIdx.x) * kPerBlock + wave / WAVES;
   if (row >= rows) return;
   const int64_t t = row / Hq;
   if (t < batch.cu[0] || t >= batch.cu[batch.B]) return;      // a row of no sequence: left as it is
-  float top = kNothing, sum = 0.0f;
-  for (int s = 0; s < splits; ++s) top = fmaxf(top, stats[s * rows + row].x);
-  for (int s = 0; s < splits; ++s) {
+  float top = kNothing;
+  for (int s = lane; s < splits; s += 64) top = fmaxf(top, stats[s * rows + row].x);
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+  float sum = 0.0f;
+  for (int s = lane; s < splits; s += 64) {
     const float2 st = stats[s * rows + row];
     sum += st.y * __builtin_amdgcn_exp2f(st.x - top);
   }
-  const float div = sum == 0.0f ? 0.0f : 1.0f / sum;
-  for (int d = (threadIdx.x & 63) * 4; d < D; d += 256) {
-    float4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < splits; ++s) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
+  const float over_l = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int first = WAVES == 1 ? 0 : wave;
+  float4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int d = lane * 4;                                     // D <= 256: a wave holds a row
+  if (d < D) {
+#pragma unroll 4
+    for (int s = first; s < splits; s += WAVES) {
       const float2 st = stats[s * rows + row];
-      if (st.y == 0.0f) continue;
-      const float f = __builtin_amdgcn_exp2f(st.x - top);
+      const float f = st.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(st.x - top);
       const float4_t p = *reinterpret_cast<const float4_t*>(partial + (s * rows + row) * D + d);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(p[i], f, v[i]);
+      for (int i = 0; i < 4; ++i) v[i] = st.y == 0.0f ? v[i] : __builtin_fmaf(p[i], f, v[i]);
     }
-    uint2_t w;
-    w[0] = uint32_t(f32_to_bf16(v[0] * div)) | (uint32_t(f32_to_bf16(v[1] * div)) << 16);
-    w[1] = uint32_t(f32_to_bf16(v[2] * div)) | (uint32_t(f32_to_bf16(v[3] * div)) << 16);
-    *reinterpret_cast<uint2_t*>(out + row * D + d) = w;
   }
+  if constexpr (WAVES > 1) {
+    part[wave][lane] = v;
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int k = 1; k < WAVES; ++k) v += part[k][lane];
+  }
+  if (d < D) *reinterpret_cast<uint2_t*>(out + row * D + d) = pack_bf16x4(v, over_l);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -625,22 +984,28 @@ unsigned page_slots(int64_t max_new, int page) {
   return unsigned(std::min<int64_t>(ceil_div(std::max<int64_t>(max_new, 1) - 1, page) + 1, 65535));
 }
 
-template <typename TIn, int DT, int RT, bool SHARE>
-hipError_t run_attention(const AttentionArgs& a, const Kv8Batch& b, const Kv8Cache& c, const Kv8Plan& p,
-                         hipStream_t stream) {
-  const int64_t groups = b.B * c.H * p.row_blocks * p.splits;
-  return launch_kernel(attention_kernel<TIn, DT, RT, SHARE>, dim3(unsigned(groups)), dim3(256), 0, stream, a,
-                       b, c);
+template <typename Kernel>
+hipError_t run_kernel(Kernel* kernel, int64_t groups, int threads, size_t lds, const AttentionArgs& a,
+                      const Kv8Batch& b, const Kv8Cache& c, hipStream_t stream) {
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
+    if (e != hipSuccess) return e;
+  }
+  return launch_kernel(kernel, dim3(unsigned(groups)), dim3(threads), lds, stream, a, b, c);
 }
 
 template <typename TIn, int DT>
 hipError_t run_attention(const AttentionArgs& a, const Kv8Batch& b, const Kv8Cache& c, const Kv8Plan& p,
                          hipStream_t stream) {
-  constexpr int kMost = DT == 256 ? 2 : 4;
-  if (!p.share) return run_attention<TIn, DT, kMost, false>(a, b, c, p, stream);
-  if (p.row_tiles == 1) return run_attention<TIn, DT, 1, true>(a, b, c, p, stream);
-  if (p.row_tiles == 2) return run_attention<TIn, DT, 2, true>(a, b, c, p, stream);
-  return run_attention<TIn, DT, kMost, true>(a, b, c, p, stream);
+  constexpr int RT = DT == 256 ? 1 : 2;
+  const int64_t groups = b.B * c.H * p.row_blocks * p.splits;
+  if (p.row_tiles == 1)
+    return run_kernel(few_rows_kernel<TIn, DT, 1>, groups, 256, few_rows_lds_bytes<DT, 1>(), a, b, c, stream);
+  if constexpr (DT < 256)
+    if (p.row_tiles == 2)
+      return run_kernel(few_rows_kernel<TIn, DT, 2>, groups, 256, few_rows_lds_bytes<DT, 2>(), a, b, c, stream);
+  return run_kernel(many_rows_kernel<TIn, DT, RT>, groups, 512, many_rows_lds_bytes<DT>(), a, b, c, stream);
 }
 
 template <typename TIn>
@@ -680,14 +1045,14 @@ Kv8Plan plan_kv8_attention(int64_t B, int64_t T, int64_t Hq, int64_t H, int64_t 
                            int64_t max_len) {
   Kv8Plan p{};
   const int64_t rows = std::max<int64_t>(std::min(max_new, T), 1) * (Hq / H);
-  const int most = D > 128 ? 2 : 4;
-  p.row_tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : most;
-  p.share = rows <= 64 * most;      // up to four workgroups' rows: tokens over the waves
-  p.row_blocks = ceil_div(rows, (p.share ? 16 : 64) * p.row_tiles);
-  // about three workgroups a compute unit, each with at least four blocks of 64 tokens
+  const bool many = rows > (D > 128 ? 16 : 32);
+  p.row_tiles = rows <= 16 ? 1 : !many ? 2 : D > 128 ? 8 : 16;
+  p.row_blocks = ceil_div(rows, 16 * p.row_tiles);
+  // tokens are split while there are too few workgroups to fill the chip: about three a compute
+  // unit for few rows, one for many, and at least four blocks of 64 tokens for each (wave)
   const int64_t groups = B * H * p.row_blocks;
-  const int64_t most_splits = std::max<int64_t>(1, max_len / (p.share ? 256 : 512));
-  p.splits = int(std::min<int64_t>(std::max<int64_t>(1, 768 / groups), std::min<int64_t>(most_splits, 256)));
+  const int64_t most = std::max<int64_t>(1, max_len / 256);
+  p.splits = int(std::min<int64_t>(std::max<int64_t>(1, (many ? 256 : 768) / groups), std::min<int64_t>(most, 256)));
   if (p.splits > 1)
     p.bytes = round256(size_t(p.splits) * T * Hq * D * 4) + round256(size_t(p.splits) * T * Hq * 8);
   return p;
@@ -716,8 +1081,12 @@ hipError_t launch_kv8_attention(const void* q, int dtype, int64_t q_t, int64_t q
   const hipError_t e = dtype == 0 ? run_attention<float>(a, b, c, p, stream)
                                   : run_attention<uint16_t>(a, b, c, p, stream);
   if (e != hipSuccess || p.splits == 1) return e;
-  return launch_kernel(join_splits_kernel, dim3(unsigned(ceil_div(a.rows, 4))), dim3(256), 0, stream, b, int(Hq),
-                       c.D, p.splits, a.rows, a.partial, a.stats, out);
+  // a wave to a row; four where there are many splits
+  if (p.splits <= 8)
+    return launch_kernel(join_splits_kernel<1>, dim3(unsigned(ceil_div(a.rows, 4))), dim3(256), 0, stream, b,
+                         int(Hq), c.D, p.splits, a.rows, a.partial, a.stats, out);
+  return launch_kernel(join_splits_kernel<4>, dim3(unsigned(a.rows)), dim3(256), 0, stream, b, int(Hq), c.D,
+                       p.splits, a.rows, a.partial, a.stats, out);
 }
 
 }  // namespace convrot

@@ -9,6 +9,7 @@ tensors' device, there is no CPU path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional, Tuple
 
@@ -16,13 +17,54 @@ import torch
 
 from . import _lib
 from ._lib import (_CODE_BYTES, _activations, _check, _codes_2d, _dtype_code, _is_tensor, _mat, _ptr,
-                   _require_device, _stream, _vec, _workspace, load_library)
+                   _require_device, _vec, _workspace, load_library)
 from .linear import _ConvLinearBase
+
+
+def _launch(fn, dev: torch.device, *args) -> int:
+    """Calls an entry point whose last argument is the stream, with the tensors' device current."""
+    index = dev.index
+    if torch._C._cuda_getDevice() == index:
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
+
+
+def _device(*ts) -> torch.device:
+    """The one GPU that all tensors (None passes) are on."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        d = t.device
+        if dev is None:
+            dev = d
+            if d.type != "cuda":
+                break
+        elif d != dev:
+            break
+    else:
+        return dev
+    return _require_device(*ts)             # says what is wrong
+
+
+def _exactly(t, name: str, shape, dtype) -> None:
+    """A contiguous tensor of this shape and dtype."""
+    if not isinstance(t, torch.Tensor):
+        _is_tensor(t, name)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
 
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "bands": 3}
 
 
 # ------------------------------------------------------------------ linear, group scales
+@functools.lru_cache(maxsize=1024)
 def convrot_w4a16_padded_k(K: int, g: int, sg: int) -> int:
     r = int(load_library().convrot_w4a16_padded_k(int(K), int(g), int(sg)))
     if r < 0:
@@ -30,6 +72,7 @@ def convrot_w4a16_padded_k(K: int, g: int, sg: int) -> int:
     return r
 
 
+@functools.lru_cache(maxsize=4096)
 def convrot_w4a16_workspace_bytes(M: int, N: int, K: int, g: int, sg: int) -> int:
     return int(load_library().convrot_w4a16_workspace_bytes(int(M), int(N), int(K), int(g), int(sg)))
 
@@ -41,14 +84,13 @@ def convrot_quant_weight_g4(w: torch.Tensor, g: int, sg: int, wq: Optional[torch
     Kp = convrot_w4a16_padded_k(K, g, sg)
     _mat(wq, "wq", N, Kp // 2, _CODE_BYTES)
     _mat(ws, "ws", N, Kp // sg, (torch.bfloat16,))
-    dev = _require_device(w, wq, ws)
+    dev = _device(w, wq, ws)
     if wq is None:
         wq = torch.empty((N, Kp // 2), dtype=torch.uint8, device=dev)
     if ws is None:
         ws = torch.empty((N, Kp // sg), dtype=torch.bfloat16, device=dev)
-    with torch.cuda.device(dev):
-        st = load_library().convrot_quant_weight_g4(_ptr(w), _dtype_code(w), N, K, g, sg, _ptr(wq),
-                                                    _ptr(ws), _stream(dev))
+    st = _launch(load_library().convrot_quant_weight_g4, dev, _ptr(w), _dtype_code(w), N, K, g, sg, _ptr(wq),
+                 _ptr(ws))
     _check(st, g)
     return wq, ws
 
@@ -64,25 +106,27 @@ def convrot_w4a16_linear(x: torch.Tensor, g: int, sg: int, wq: torch.Tensor, ws:
     if cols != Kp // 2:
         raise ValueError(f"wq must have {Kp // 2} bytes per row for K={K}, g={g}, sg={sg} (K' = {Kp}), "
                          f"got {cols}")
-    _mat(wq, "wq", N, cols, _CODE_BYTES)
-    _is_tensor(ws, "ws")
-    _mat(ws, "ws", N, Kp // sg, (torch.bfloat16,))
-    _vec(bias, "bias", N, torch.bfloat16)
-    _mat(y, "y", M, N, (torch.bfloat16,))
+    if wq.dtype is not torch.uint8 or not wq.is_contiguous():
+        _mat(wq, "wq", N, cols, _CODE_BYTES)
+    _exactly(ws, "ws", (N, Kp // sg), torch.bfloat16)
+    if bias is not None:
+        _vec(bias, "bias", N, torch.bfloat16)
+    if y is not None:
+        _exactly(y, "y", (M, N), torch.bfloat16)
     if workspace is not None:
         _workspace(workspace)
-    dev = _require_device(x, wq, ws, bias, y, workspace)
+    dev = _device(x, wq, ws, bias, y, workspace)
     if workspace is None:
         need = convrot_w4a16_workspace_bytes(M, N, K, g, sg)
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
     if y is None:
         y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
     ldx = x.stride(0) if M > 1 else K                      # one row has no stride
-    with torch.cuda.device(dev):
-        st = load_library().convrot_w4a16_linear(
-            _ptr(x), _dtype_code(x), M, K, ldx, g, sg, _ptr(wq), _ptr(ws), N, _ptr(bias), _ptr(y),
-            _ptr(workspace), 0 if workspace is None else _workspace(workspace), _stream(dev))
-    _check(st, g)
+    st = _launch(load_library().convrot_w4a16_linear, dev, x.data_ptr(), _dtype_code(x), M, K, ldx, g, sg,
+                 wq.data_ptr(), ws.data_ptr(), N, _ptr(bias), y.data_ptr(), _ptr(workspace),
+                 0 if workspace is None else _workspace(workspace))
+    if st:
+        _check(st, g)
     return y
 
 
@@ -102,13 +146,15 @@ def convrot_rotary_frequencies(R: int, base: float = 10000.0, scaling: str = "pl
 
 def _heads(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
     """A [tokens, heads, D] tensor with the elements of a head next to each other."""
-    _is_tensor(t, name)
+    if not isinstance(t, torch.Tensor):
+        _is_tensor(t, name)
     if t.dim() != 3:
         raise ValueError(f"{name} must be 3-D [tokens, heads, head size], got {t.dim()} dimensions")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    T, H, D = t.shape
+    if D > 1 and t.stride(2) != 1:
         raise ValueError(f"{name} must have its heads' elements contiguous")
     _dtype_code(t)
-    return tuple(int(v) for v in t.shape)
+    return T, H, D
 
 
 def _span(t: torch.Tensor) -> Tuple[int, int]:
@@ -143,66 +189,61 @@ def convrot_rotary(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor
                              f"{tuple(k.shape)} and {k.dtype}")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _is_tensor(pos, "pos")
+    _exactly(pos, "pos", (T,), torch.int64)
     _is_tensor(inv_freq, "inv_freq")
-    _vec(pos, "pos", T, torch.int64)
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be 1-D")
-    _vec(inv_freq, "inv_freq", inv_freq.shape[0], torch.float32)
+    _exactly(inv_freq, "inv_freq", inv_freq.shape, torch.float32)
     _rotary_out(q, q_out, "q_out")
     if k is not None:
         _rotary_out(k, k_out, "k_out")
-    dev = _require_device(q, k, pos, inv_freq, q_out, k_out)
+    dev = _device(q, k, pos, inv_freq, q_out, k_out)
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     if k is not None and k_out is None:
         k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
-    part = lambda t, o: (_ptr(t), t.stride(0), t.stride(1), _ptr(o), o.stride(0), o.stride(1), t.shape[1])  # noqa: E731
-    with torch.cuda.device(dev):
-        st = load_library().convrot_rotary(
-            *part(q, q_out), *(part(k, k_out) if k is not None else (None, 0, 0, None, 0, 0, 0)),
-            _dtype_code(q), T, D, 2 * inv_freq.shape[0], _ptr(pos), _ptr(inv_freq), int(bool(interleaved)),
-            float(factor), int(bool(inverse)), _stream(dev))
-    _check(st)
+    part = lambda t, o: (t.data_ptr(), *t.stride()[:2], o.data_ptr(), *o.stride()[:2], t.shape[1])  # noqa: E731
+    st = _launch(load_library().convrot_rotary, dev, *part(q, q_out),
+                 *(part(k, k_out) if k is not None else (None, 0, 0, None, 0, 0, 0)),
+                 _dtype_code(q), T, D, 2 * inv_freq.shape[0], pos.data_ptr(), inv_freq.data_ptr(),
+                 int(bool(interleaved)), factor, int(bool(inverse)))
+    if st:
+        _check(st)
     return q_out, k_out
 
 
 # ----------------------------------------------------------------------- 8-bit paged cache
 def _batch(cu, lens, table):
-    for t, name in ((cu, "cu"), (lens, "lens"), (table, "table")):
-        _is_tensor(t, name)
+    _is_tensor(lens, "lens")
     if lens.dim() != 1:
         raise ValueError("lens must be 1-D")
-    B = int(lens.shape[0])
-    _vec(cu, "cu", B + 1, torch.int32)
-    _vec(lens, "lens", B, torch.int32)
-    if table.dtype != torch.int32:
+    B = lens.shape[0]
+    _exactly(cu, "cu", (B + 1,), torch.int32)
+    _exactly(lens, "lens", (B,), torch.int32)
+    _is_tensor(table, "table")
+    if table.dtype is not torch.int32:
         raise TypeError(f"table must be torch.int32, got {table.dtype}")
     if table.dim() != 2 or table.shape[0] != B:
         raise ValueError(f"table must have shape ({B}, pages), got {tuple(table.shape)}")
-    if table.shape[1] > 1 and table.stride(1) != 1:
+    width = table.shape[1]
+    if width > 1 and table.stride(1) != 1:
         raise ValueError("table must have contiguous rows")
-    if B > 1 and table.stride(0) < table.shape[1]:
+    ld = table.stride(0) if B > 1 else width
+    if ld < width:
         raise ValueError("rows of table must not overlap")
-    ld = table.stride(0) if B > 1 else table.shape[1]
-    return B, (_ptr(cu), _ptr(lens), _ptr(table), ld, B, table.shape[1])
+    return B, (cu.data_ptr(), lens.data_ptr(), table.data_ptr(), ld, B, width)
 
 
 def _cache(kc, ks, vc, vs, g):
-    for t, name in ((kc, "kc"), (ks, "ks"), (vc, "vc"), (vs, "vs")):
-        _is_tensor(t, name)
+    _is_tensor(kc, "kc")
     if kc.dim() != 4:
         raise ValueError(f"kc must be 4-D [pages, heads, page, head size], got {kc.dim()} dimensions")
-    P, H, page, D = (int(v) for v in kc.shape)
-    for t, name, shape, dtype in ((kc, "kc", (P, H, page, D), torch.int8), (ks, "ks", (P, H), torch.float32),
-                                  (vc, "vc", (P, H, D, page), torch.int8), (vs, "vs", (P, H), torch.float32)):
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    return H, page, D, (_ptr(kc), _ptr(ks), _ptr(vc), _ptr(vs), P, page, H, D, int(g))
+    P, H, page, D = kc.shape
+    _exactly(kc, "kc", kc.shape, torch.int8)
+    _exactly(ks, "ks", (P, H), torch.float32)
+    _exactly(vc, "vc", (P, H, D, page), torch.int8)
+    _exactly(vs, "vs", (P, H), torch.float32)
+    return H, page, D, (kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), P, page, H, D, g)
 
 
 def convrot_kv8_append(k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor,
@@ -218,12 +259,11 @@ def convrot_kv8_append(k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, lens:
     cH, page, cD, cache = _cache(kc, ks, vc, vs, g)
     if (cH, cD) != (H, D):
         raise ValueError(f"k has {H} heads of {D}, the cache {cH} of {cD}")
-    dev = _require_device(k, v, cu, lens, table, kc, ks, vc, vs)
-    with torch.cuda.device(dev):
-        st = load_library().convrot_kv8_append(
-            _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1), _dtype_code(k), T, *batch,
-            *cache, T if max_new is None else int(max_new), _stream(dev))
-    _check(st, g)
+    dev = _device(k, v, cu, lens, table, kc, ks, vc, vs)
+    st = _launch(load_library().convrot_kv8_append, dev, k.data_ptr(), *k.stride()[:2], v.data_ptr(),
+                 *v.stride()[:2], _dtype_code(k), T, *batch, *cache, T if max_new is None else max_new)
+    if st:
+        _check(st, g)
 
 
 def convrot_kv8_read(cu: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, kc: torch.Tensor,
@@ -248,15 +288,16 @@ def convrot_kv8_read(cu: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, 
     tokens = int(tokens)
     if tokens < 0:
         raise ValueError(f"tokens must not be negative, got {tokens}")
-    dev = _require_device(cu, lens, table, kc, ks, vc, vs, k, v)
+    dev = _device(cu, lens, table, kc, ks, vc, vs, k, v)
     k, v = (torch.empty((tokens, H, D), dtype=torch.bfloat16, device=dev) if t is None else t for t in (k, v))
-    with torch.cuda.device(dev):
-        st = load_library().convrot_kv8_read(*batch, *cache, tokens if max_new is None else int(max_new), tokens,
-                                             _ptr(k), _ptr(v), _stream(dev))
-    _check(st, g)
+    st = _launch(load_library().convrot_kv8_read, dev, *batch, *cache, tokens if max_new is None else max_new,
+                 tokens, k.data_ptr(), v.data_ptr())
+    if st:
+        _check(st, g)
     return k, v
 
 
+@functools.lru_cache(maxsize=4096)
 def convrot_kv8_attention_workspace_bytes(T: int, B: int, Hq: int, H: int, D: int, max_new: int,
                                           max_len: int) -> int:
     return int(load_library().convrot_kv8_attention_workspace_bytes(
@@ -282,20 +323,19 @@ def convrot_kv8_attention(q: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor,
             raise ValueError(f"out must be contiguous bfloat16 with shape {(T, Hq, D)}, got {tuple(out.shape)}, {out.dtype}")
     if workspace is not None:
         _workspace(workspace)
-    dev = _require_device(q, cu, lens, table, kc, ks, vc, vs, out, workspace)
-    max_new = T if max_new is None else int(max_new)
-    max_len = int(table.shape[1]) * page if max_len is None else int(max_len)
+    dev = _device(q, cu, lens, table, kc, ks, vc, vs, out, workspace)
+    max_new = T if max_new is None else max_new
+    max_len = table.shape[1] * page if max_len is None else max_len
     if workspace is None:
         need = convrot_kv8_attention_workspace_bytes(T, B, Hq, H, D, max_new, max_len)
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
     if out is None:
         out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-    with torch.cuda.device(dev):
-        st = load_library().convrot_kv8_attention(
-            _ptr(q), q.stride(0), q.stride(1), _dtype_code(q), T, Hq, *batch, *cache,
-            1.0 / math.sqrt(D) if scale is None else float(scale), max_new, max_len, _ptr(out),
-            _ptr(workspace), 0 if workspace is None else _workspace(workspace), _stream(dev))
-    _check(st, g)
+    st = _launch(load_library().convrot_kv8_attention, dev, q.data_ptr(), *q.stride()[:2], _dtype_code(q), T, Hq,
+                 *batch, *cache, 1.0 / math.sqrt(D) if scale is None else scale, max_new, max_len, out.data_ptr(),
+                 _ptr(workspace), 0 if workspace is None else _workspace(workspace))
+    if st:
+        _check(st, g)
     return out
 
 
