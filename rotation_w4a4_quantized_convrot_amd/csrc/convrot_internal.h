@@ -125,7 +125,7 @@ hipError_t launch_kv8_read(const Kv8Batch& b, const Kv8Cache& c, int g, int64_t 
 
 // Attention over it: how the work is split, and the workspace that needs.
 struct Kv8Plan {
-  int row_tiles;       // 16-row tiles of a workgroup: 1 or 2 (few rows), 8 or 16 (many)
+  int row_tiles;       // 16-row tiles of a workgroup: 1, 2 or 4 (few rows), 8 or 16 (many)
   int64_t row_blocks;  // per sequence and cached head
   int splits;          // of a sequence's tokens
   size_t bytes;

@@ -268,13 +268,19 @@ __device__ __forceinline__ half8 pack_half8(const float4_t& a, const float4_t& b
   return half8{p[0], p[1], q[0], q[1], r[0], r[1], s[0], s[1]};
 }
 
+// Over the four lane rows (lanes 16 apart): swapping a register with itself gives a lane its own value
+// and that of the lane 16, or 32, away, without LDS.
 __device__ __forceinline__ float max_over_lane_rows(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
 }
 __device__ __forceinline__ float sum_over_lane_rows(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
 
 // A barrier for what is in LDS: loads from memory may still be on their way.
@@ -394,7 +400,7 @@ __device__ __forceinline__ PageScale scale_of(const Pages& p, int32_t id, uint32
   return PageScale{p.ks[at], p.vs[at], p.there(id, base, off)};
 }
 
-// A block of 64 scores a row (16 of them in each lane) to weights, with the running reference m, sum l
+// A block of 64 scores a row (16 of them in each lane) becomes weights, with a running reference m, sum l
 // and output o of each row.  With s_j = scale q.k_j in powers of two, vs_j the page's value scale and
 // R the reference, at most kSlack below max(s_j + log2 vs_j):
 //   w_j = 2^(s_j + log2 vs_j - R + kShift),   o = sum w_j vcode_j,   l = sum w_j / vs_j,
@@ -402,35 +408,49 @@ __device__ __forceinline__ PageScale scale_of(const Pages& p, int32_t id, uint32
 // rounded to fp16 (2^-12 relative; below 2^-21 of the reference an absolute 2^-32 of it) uses that
 // type's range.  The reference moves only when a score passes it by 2^kSlack, so that o is rarely
 // scaled again.
-// `ragged`: some token of the block is not there or not seen by some row; token (the lane's first),
-// limit and sees (a row's last token) count from the share's first token.
+struct BlockScale {
+  float ks, lv, over_vs;
+  // bit 0: the lane's 16 tokens have no page; 1: their values' scale is 0; 2 and 3: so it is for some lane
+  int bits;
+};
+
+__device__ __forceinline__ BlockScale settle(const PageScale& page) {
+  const bool zero = page.vs == 0.0f;
+  const float lv = zero ? 0.0f : __builtin_amdgcn_logf(page.vs);
+  return BlockScale{page.ks, lv, __builtin_amdgcn_exp2f(-lv),
+                    (page.there ? 0 : 1) | (zero ? 2 : 0) | (__any(!page.there) ? 4 : 0) | (__any(zero) ? 8 : 0)};
+}
+
+// First half: scores of tokens that are not there or not seen to -infinity (`ragged`: there are some;
+// token, the lane's first, limit and sees, a row's last token, count from the share's first), and the
+// references.
 template <int RT, int TILES>
-__device__ __forceinline__ void weigh(float4_t (&s)[4][RT], const PageScale& page, bool ragged, int token,
-                                      int limit, const float (&row_scale)[RT], const int (&sees)[RT],
-                                      float (&m)[RT], float (&l)[RT], float4_t (&o)[TILES][RT], half8 (&w0)[RT],
-                                      half8 (&w1)[RT]) {
-  const float lv = page.vs == 0.0f ? 0.0f : __builtin_amdgcn_logf(page.vs);
-  const float over_vs = __builtin_amdgcn_exp2f(-lv);
-  const bool no_values = __any(page.vs == 0.0f);
-  float mul[RT], high[RT];
+__device__ __forceinline__ void refer(float4_t (&s)[4][RT], const BlockScale& bs, bool ragged, int token, int limit,
+                                      const float (&row_scale)[RT], const int (&sees)[RT], float (&m)[RT],
+                                      float (&l)[RT], float4_t (&o)[TILES][RT], float (&mul)[RT]) {
+  if (ragged) {
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    mul[rt] = row_scale[rt] * page.ks;
-    if (ragged) {
-      const int seen = page.there ? min(sees[rt], limit - 1) - token : -1;
+    for (int rt = 0; rt < RT; ++rt) {
+      const int seen = bs.bits & 1 ? -1 : min(sees[rt], limit - 1) - token;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (4 * t + i > seen) s[t][rt][i] = -INFINITY;
     }
-    float top = s[0][rt][0];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) top = fmaxf(top, s[t][rt][i]);
-    high[rt] = fmaxf(kNothing, max_over_lane_rows(top * mul[rt] + lv));
   }
+  float high[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    mul[rt] = row_scale[rt] * bs.ks;
+    float top[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) top[t] = fmaxf(fmaxf(s[t][rt][0], s[t][rt][1]), fmaxf(s[t][rt][2], s[t][rt][3]));
+    top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    high[rt] = fmaxf(kNothing, top[0] * mul[rt] + bs.lv);
+  }
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) high[rt] = max_over_lane_rows(high[rt]);
   bool grown = false;
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) grown = grown || high[rt] > m[rt] + kSlack;
@@ -445,24 +465,43 @@ __device__ __forceinline__ void weigh(float4_t (&s)[4][RT], const PageScale& pag
       for (int dt = 0; dt < TILES; ++dt) o[dt][rt] *= down;
     }
   }
+}
+
+// Second half: the weights, in the layout of the second product's operand.
+template <bool RAGGED, int RT>
+__device__ __forceinline__ void weigh(const float4_t (&s)[4][RT], const BlockScale& bs, const float (&mul)[RT],
+                                      const float (&m)[RT], float (&l)[RT], half8 (&w0)[RT], half8 (&w1)[RT]) {
+  float4_t w[4][RT];
+  float add[RT];
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const float add = lv - m[rt] + kShift;
-    float sum = 0.0f;
+  for (int rt = 0; rt < RT; ++rt) add[rt] = bs.lv - m[rt] + kShift;
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][rt][i], mul[rt], add));
-        if (ragged && s[t][rt][i] == -INFINITY) w = 0.0f;      // also where mul or add is NaN
-        s[t][rt][i] = w;
-        sum += w;
+        w[t][rt][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][rt][i], mul[rt], add[rt]));
+        if (RAGGED && s[t][rt][i] == -INFINITY) w[t][rt][i] = 0.0f;     // also where mul or add is NaN
       }
-    l[rt] += sum == 0.0f ? 0.0f : sum * over_vs;
-    w0[rt] = pack_half8(s[0][rt], s[1][rt]);
-    w1[rt] = pack_half8(s[2][rt], s[3][rt]);
-    if (no_values && page.vs == 0.0f) w0[rt] = w1[rt] = half8{};
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    float4_t part;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part[i] = (w[0][rt][i] + w[1][rt][i]) + (w[2][rt][i] + w[3][rt][i]);
+    const float sum = (part[0] + part[1]) + (part[2] + part[3]);
+    l[rt] += sum == 0.0f ? 0.0f : sum * bs.over_vs;
+    w0[rt] = pack_half8(w[0][rt], w[1][rt]);
+    w1[rt] = pack_half8(w[2][rt], w[3][rt]);
   }
+}
+
+// Values of a page whose scale is 0 count as zeros, whatever their codes.
+template <int RT>
+__device__ __forceinline__ void drop_zero_values(const BlockScale& bs, half8 (&w0)[RT], half8 (&w1)[RT]) {
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+    if (bs.bits & 2) w0[rt] = w1[rt] = half8{};
 }
 
 __device__ __forceinline__ uint2_t pack_bf16x4(const float4_t& v, float mul) {
@@ -485,25 +524,28 @@ __device__ __forceinline__ void put(const AttentionArgs& a, int D, int64_t split
 // operand needs, so the weights never leave the registers; the row statistics need two lane
 // exchanges a block.  Rows are (query, head of the group) pairs of one cached head.
 
-// Few rows (up to 16 * RT of a cached head): the four waves of a workgroup take every fourth block of
-// tokens, straight from memory into their registers, and add up through LDS at the end.  The cache's
+// Few rows: a workgroup takes 16 * TILES rows of a cached head, each of its four waves 16 of them and
+// every (4 / TILES)th block of tokens, straight from memory into its registers (waves with the same
+// tokens find them in the L1 cache); the waves of a tile add up through LDS at the end.  The cache's
 // bytes are the bound: a block's keys are asked for as soon as the last block's are used, its values as
 // soon as those are.
-template <int DT, int RT>
+template <int DT>
 constexpr size_t few_rows_lds_bytes() {
-  return size_t(4) * 16 * RT * (DT + 4) * 4;
+  return size_t(4) * 16 * (DT + 4) * 4;
 }
 
-template <typename TIn, int DT, int RT>
-__global__ __launch_bounds__(256, DT * RT <= 128 ? 2 : 1) void few_rows_kernel(AttentionArgs a, Kv8Batch batch, Kv8Cache cache) {
-  constexpr int kRows = RT * 16, kQStride = DT + 8, kPieces = DT / 64, kTilesD = DT / 16;
+template <typename TIn, int DT, int TILES>
+__global__ __launch_bounds__(256, DT <= 128 ? 2 : 1) void few_rows_kernel(AttentionArgs a, Kv8Batch batch, Kv8Cache cache) {
+  constexpr int RT = 1, kPhases = 4 / TILES, kStep = 64 * kPhases;
+  constexpr int kRows = TILES * 16, kQStride = DT + 8, kPieces = DT / 64, kTilesD = DT / 16;
   constexpr int kOStride = DT + 4;
   extern __shared__ __align__(16) uint8_t lds[];     // few_rows_lds_bytes: the queries, later the sums
   __shared__ float factor[kRows];
-  __shared__ float wave_m[4][kRows], wave_l[4][kRows];
+  __shared__ float wave_m[4][16], wave_l[4][16];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, c = lane >> 4;
+  const int tile = wave % TILES, phase = wave / TILES;
   const Work w = work_of(a, batch, cache);
   const int G = a.Hq / cache.H;
   _Float16* const q_lds = reinterpret_cast<_Float16*>(lds);
@@ -522,13 +564,13 @@ __global__ __launch_bounds__(256, DT * RT <= 128 ? 2 : 1) void few_rows_kernel(A
     // tokens of a block that concern the lane: the 16 whose keys it loads (16 (n / 4) ...), and the 16
     // whose values and scores it holds (16 c ...)
     const Pages pages = pages_of(batch, cache, w, limit);
-    const uint32_t off_k = 16 * (n >> 2), off_v = 16 * c, base0 = uint32_t(from) * 64 + wave * 64;
+    const uint32_t off_k = 16 * (n >> 2), off_v = 16 * c, base0 = uint32_t(from) * 64 + phase * 64;
     int32_t idk = -1, idv = -1, idk1 = -1, idv1 = -1;            // of the first block and the next
-    if (wave < count) {
+    if (phase < count) {
       idk = pages.find(base0, off_k);
       idv = pages.find(base0, off_v);
-      idk1 = pages.find(base0 + 256, off_k);
-      idv1 = pages.find(base0 + 256, off_v);
+      idk1 = pages.find(base0 + kStep, off_k);
+      idv1 = pages.find(base0 + kStep, off_v);
     }
     __syncthreads();
     for (int i = wave * 4 + c; i < kRows; i += 16)
@@ -554,7 +596,7 @@ __global__ __launch_bounds__(256, DT * RT <= 128 ? 2 : 1) void few_rows_kernel(A
       }
     };
     PageScale page{};
-    if (wave < count) {
+    if (phase < count) {
       load_keys(base0, idk);
       page = scale_of(pages, idv, base0, off_v);
       load_values(base0, idv);
@@ -573,9 +615,9 @@ __global__ __launch_bounds__(256, DT * RT <= 128 ? 2 : 1) void few_rows_kernel(A
       for (int p = 0; p < kPieces; ++p)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          q[rt][p][k] = *reinterpret_cast<const half8*>(&q_lds[(rt * 16 + n) * kQStride + 64 * p + 16 * c + 8 * k]);
-      const int64_t r = r0 + rt * 16 + n;
-      row_scale[rt] = factor[rt * 16 + n];
+          q[rt][p][k] = *reinterpret_cast<const half8*>(&q_lds[(tile * 16 + n) * kQStride + 64 * p + 16 * c + 8 * k]);
+      const int64_t r = r0 + tile * 16 + n;
+      row_scale[rt] = factor[tile * 16 + n];
       sees[rt] = r < w.rows ? from_here(w.before + r / G, from * 64) : -1;
       m[rt] = kNothing;
       l[rt] = 0.0f;
@@ -604,15 +646,21 @@ __global__ __launch_bounds__(256, DT * RT <= 128 ? 2 : 1) void few_rows_kernel(A
             for (int rt = 0; rt < RT; ++rt)
               s[t][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q[rt][p][k], s[t][rt], 0, 0, 0);
           }
-      const uint32_t ahead = uint32_t(from + blk + 4) * 64;
+      const uint32_t ahead = uint32_t(from + blk + kPhases) * 64;
       if constexpr (more) {
         load_keys(ahead, idk);
-        idk = pages.find(ahead + 256, off_k);
+        idk = pages.find(ahead + kStep, off_k);
       }
       __builtin_amdgcn_sched_barrier(0);
-      const bool ragged = base + 63 > all_see || base + 64 > rel_limit || __any(!page.there);
+      const BlockScale bs = settle(page);
+      const int some = __builtin_amdgcn_readfirstlane(bs.bits);
+      const bool ragged = base + 63 > all_see || base + 64 > rel_limit || (some & 4);
       half8 w0[RT], w1[RT];
-      weigh(s, page, ragged, base + 16 * c, rel_limit, row_scale, sees, m, l, o, w0, w1);
+      float mul[RT];
+      refer(s, bs, ragged, base + 16 * c, rel_limit, row_scale, sees, m, l, o, mul);
+      if (ragged) weigh<true>(s, bs, mul, m, l, w0, w1);
+      else weigh<false>(s, bs, mul, m, l, w0, w1);
+      if (some & 8) drop_zero_values(bs, w0, w1);
       if constexpr (more) page = scale_of(pages, idv, ahead, off_v);
 #pragma unroll
       for (int k = 0; k < 2; ++k)
@@ -625,84 +673,75 @@ __global__ __launch_bounds__(256, DT * RT <= 128 ? 2 : 1) void few_rows_kernel(A
         }
       if constexpr (more) {
         load_values(ahead, idv);
-        idv = pages.find(ahead + 256, off_v);
+        idv = pages.find(ahead + kStep, off_v);
       }
       __builtin_amdgcn_sched_barrier(0);
     };
-    int blk = wave;
-    for (; blk + 4 < count; blk += 4) step(std::true_type{}, blk);
+    int blk = phase;
+    for (; blk + kPhases < count; blk += kPhases) step(std::true_type{}, blk);
     if (blk < count) step(std::false_type{}, blk);
 
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) l[rt] = sum_over_lane_rows(l[rt]);
-    // the four waves' sums, added in wave order
+    // the sums of a tile's waves, added in their order
     if (c == 0) {
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        wave_m[wave][rt * 16 + n] = m[rt];
-        wave_l[wave][rt * 16 + n] = l[rt];
-      }
+      wave_m[wave][n] = m[0];
+      wave_l[wave][n] = l[0];
     }
     __syncthreads();                // also: no wave reads the queries any more
     float* const sums = reinterpret_cast<float*>(lds);
+    const auto top_of = [&](int t, int i) {
+      float top = wave_m[t][i];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int r = rt * 16 + n;
-      const float top = fmaxf(fmaxf(wave_m[0][r], wave_m[1][r]), fmaxf(wave_m[2][r], wave_m[3][r]));
-      const float down = __builtin_amdgcn_exp2f(m[rt] - top);
+      for (int k = 1; k < kPhases; ++k) top = fmaxf(top, wave_m[t + k * TILES][i]);
+      return top;
+    };
+    const float down = __builtin_amdgcn_exp2f(m[0] - top_of(tile, n));
 #pragma unroll
-      for (int dt = 0; dt < kTilesD; ++dt)
-        *reinterpret_cast<float4_t*>(&sums[(wave * kRows + r) * kOStride + 16 * dt + 4 * c]) = o[dt][rt] * down;
-    }
+    for (int dt = 0; dt < kTilesD; ++dt)
+      *reinterpret_cast<float4_t*>(&sums[(wave * 16 + n) * kOStride + 16 * dt + 4 * c]) = o[dt][0] * down;
     __syncthreads();
     // a row of 16 lanes to a row
-    for (int i = threadIdx.x >> 4; i < kRows; i += 16) {
-      const int64_t r = r0 + i;
+    for (int k = threadIdx.x >> 4; k < kRows; k += 16) {
+      const int64_t r = r0 + k;
+      const int t = k >> 4, i = k & 15;
       if (r >= w.rows) continue;
-      const float top = fmaxf(fmaxf(wave_m[0][i], wave_m[1][i]), fmaxf(wave_m[2][i], wave_m[3][i]));
+      const float top = top_of(t, i);
       float sum = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sum += wave_l[k][i] * __builtin_amdgcn_exp2f(wave_m[k][i] - top);
+      for (int p = 0; p < kPhases; ++p)
+        sum += wave_l[t + p * TILES][i] * __builtin_amdgcn_exp2f(wave_m[t + p * TILES][i] - top);
       const int64_t row = (w.seq.row0 + r / G) * a.Hq + w.h * G + r % G;
       if (a.partial != nullptr && n == 0) a.stats[w.split * a.rows + row] = make_float2(top, sum);
       const float over_l = sum == 0.0f ? 0.0f : 1.0f / sum;
       for (int d = n * 4; d < cache.D; d += 64) {
-        float4_t v = *reinterpret_cast<const float4_t*>(&sums[i * kOStride + d]);
+        float4_t v = *reinterpret_cast<const float4_t*>(&sums[(t * 16 + i) * kOStride + d]);
 #pragma unroll
-        for (int k = 1; k < 4; ++k) v += *reinterpret_cast<const float4_t*>(&sums[(k * kRows + i) * kOStride + d]);
+        for (int p = 1; p < kPhases; ++p)
+          v += *reinterpret_cast<const float4_t*>(&sums[((t + p * TILES) * 16 + i) * kOStride + d]);
         put(a, cache.D, w.split, row, d, v, over_l);
       }
     }
   }
 }
 
-// Operand reads from LDS stay kAhead blocks ahead of the matrix instructions that use them (left
-// alone, the compiler reads each one right before its use and waits for it).
-constexpr int kAhead = 6;
-
-template <int READS, int PER>
-__device__ __forceinline__ void keep_reads_ahead() {
-  __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);       // LDS reads
-#pragma unroll
-  for (int j = kAhead; j < READS; ++j) {
-    __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);        // matrix instructions
-    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-  }
-  __builtin_amdgcn_sched_group_barrier(0x008, PER * kAhead, 0);
-}
+constexpr int kAhead = 6;      // operand reads from LDS that are ahead of their use
 
 // Many rows: a workgroup of eight waves takes 8 * 16 * RT rows.  Every block of 64 tokens is decoded
 // once, an eighth by each wave, into the operand layout in LDS (blocks of 1 KB that a wave reads as
 // they are), where all eight waves use it.
 //
 // A block is two phases of a wave, one of vector arithmetic (its weights) and one of matrix
-// instructions (its values' product, then the next block's scores).  The two waves of a SIMD, w and
-// w + 4, are kept one phase apart by a barrier after each, so that the matrix cores work for one
-// while the other has its weights computed.  With phases counted over both groups, waves 0-3 do the
-// weights of block i in phase 2 i and its products in 2 i + 1, waves 4-7 one later: keys of block j
-// are read in phases 2 j - 1 and 2 j, values in 2 j + 1 and 2 j + 2.  In its product phase of block i a
-// wave writes its part of the keys of block i + 2 and of the values of block i + 1: two buffers each
-// are enough, and four places for the page scales (read in phases 2 j and 2 j + 1, written in 2 j - 3).
+// instructions (its values' product, then the next block's scores) with the decoding of coming blocks
+// between them.  The two waves of a SIMD, w and w + 4, are kept one phase apart by a barrier after
+// each, so that the matrix cores work for one while the other has its weights computed (3x900 rows
+// over 6000 tokens: 261 us with the groups apart, 289 without; waves 2 i and 2 i + 1 apart, which share no
+// SIMD, 319); the matrix phase has the higher priority (248 against 261 us).  With phases counted
+// over both groups, waves 0-3 do the weights of block i in phase 2 i and its products in 2 i + 1, waves
+// 4-7 one later: keys of block j are read in phases 2 j - 1 and 2 j, values in 2 j + 1 and 2 j + 2.  In its
+// product phase of block i a wave writes its part of the keys of block i + 2 and of the values of block
+// i + 1: two buffers each are enough, and four places for the page scales (read in phases 2 j - 1 to
+// 2 j + 1, written in 2 j - 3 and 2 j - 2).
 template <int DT>
 constexpr size_t many_rows_lds_bytes() {
   return size_t(DT / 8) * 2048 * 2 + 4 * 64;
@@ -791,45 +830,33 @@ __global__ __launch_bounds__(512) void many_rows_kernel(AttentionArgs a, Kv8Batc
         if (works) raw_v[i] = *reinterpret_cast<const uint4_t*>(vp + (d < cache.D ? d : 0) * cache.page);
       }
     };
-    const auto write = [&](uint8_t* at, const uint4_t (&raw)[kMine]) {
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        if (!works) continue;
-        half8* const p = reinterpret_cast<half8*>(at + (i * 8 + wave) * 2048) + lane;
-        p[0] = decode_i8(raw[i][0], raw[i][1]);
-        p[64] = decode_i8(raw[i][2], raw[i][3]);
-      }
+    // half h of job i of a wave's part, decoded and written
+    const auto write = [&](uint8_t* at, const uint4_t& raw, int i, int h) {
+      if (works) reinterpret_cast<half8*>(at + (i * 8 + wave) * 2048)[64 * h + lane] = decode_i8(raw[2 * h], raw[2 * h + 1]);
     };
-    const auto write_scale = [&](int i) {
-      if (wave == 0 && n == 0) {
-        float* const p = scale_lds + (i & 3) * 16 + 4 * c;
-        p[0] = raw_page.ks;
-        p[1] = raw_page.vs;
-        p[2] = raw_page.there ? 1.0f : 0.0f;
-      }
+    const auto write_all = [&](uint8_t* at, const uint4_t (&raw)[kMine]) {
+#pragma unroll
+      for (int i = 0; i < 2 * kMine; ++i) write(at, raw[i / 2], i / 2, i % 2);
+    };
+    const auto write_scale = [&](int i) {                   // by every lane that knows it, all alike
+      const BlockScale bs = settle(raw_page);
+      reinterpret_cast<float4_t*>(scale_lds)[(i & 3) * 4 + c] = float4_t{bs.ks, bs.lv, bs.over_vs, __int_as_float(bs.bits)};
     };
     float4_t s[4][RT];
-    const auto scores = [&](int i) {
-      const uint8_t* const at = key_lds + (i & 1) * kHalf;
+    // operand blocks of the scores: piece j / 8, half j / 4 % 2, token tile j % 4; of the values' product:
+    // half j / kTilesD of the tokens, channel tile j % kTilesD
+    constexpr int kReads = 2 * kTilesD;
+    const auto key_block = [&](const uint8_t* at, int j) {
+      return reinterpret_cast<const half8*>(at + (j / 8 * 4 + j % 4) * 2048)[j / 4 % 2 * 64 + lane];
+    };
+    const auto value_block = [&](const uint8_t* at, int j) {
+      return reinterpret_cast<const half8*>(at + j % kTilesD * 2048)[j / kTilesD * 64 + lane];
+    };
+    const auto score_step = [&](const half8& key, int j) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) s[t][rt] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-      const auto fragment = [&](int j) {       // piece j / 8, half j / 4 % 2, token tile j % 4
-        return reinterpret_cast<const half8*>(at + (j / 8 * 4 + j % 4) * 2048)[j / 4 % 2 * 64 + lane];
-      };
-      half8 ring[kAhead];
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) ring[j] = fragment(j);
-#pragma unroll
-      for (int j = 0; j < 8 * kPieces; ++j) {
-        const half8 key = ring[j % kAhead];
-        if (j + kAhead < 8 * kPieces) ring[j % kAhead] = fragment(j + kAhead);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-          s[j % 4][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q[rt][j / 8][j / 4 % 2], s[j % 4][rt], 0, 0, 0);
-      }
-      keep_reads_ahead<8 * kPieces, RT>();
+      for (int rt = 0; rt < RT; ++rt)
+        s[j % 4][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+            key, q[rt][j / 8][j / 4 % 2], j < 4 ? float4_t{0.0f, 0.0f, 0.0f, 0.0f} : s[j % 4][rt], 0, 0, 0);
     };
 
     if (count > 0) {
@@ -840,12 +867,12 @@ __global__ __launch_bounds__(512) void many_rows_kernel(AttentionArgs a, Kv8Batc
       load_keys(base0, k0);
       load_values(base0, v0);
       raw_page = scale_of(pages, v0, base0, off_v);
-      write(key_lds, raw_k);
-      write(value_lds, raw_v);
+      write_all(key_lds, raw_k);
+      write_all(value_lds, raw_v);
       write_scale(0);
       load_keys(base0 + 64, k1);
       raw_page = scale_of(pages, v1, base0 + 64, off_v);
-      write(key_lds + kHalf, raw_k);
+      write_all(key_lds + kHalf, raw_k);
       write_scale(1);
       load_keys(base0 + 128, k2);
       raw_page = scale_of(pages, v2, base0 + 128, off_v);
@@ -855,48 +882,75 @@ __global__ __launch_bounds__(512) void many_rows_kernel(AttentionArgs a, Kv8Batc
       // used.
       int32_t idk = pages.find(base0 + 192, off_k), ids = pages.find(base0 + 192, off_v), idv = v2;
       lds_barrier();
-      if (active) scores(0);
+#pragma unroll
+      for (int j = 0; j < kReads; ++j) score_step(key_block(key_lds, j), j);
       if (wave >= 4) lds_barrier();
-      for (int i = 0; i < count; ++i) {
-        half8 w0[RT], w1[RT];
-        if (active) {
-          const float* const ps = scale_lds + (i & 3) * 16 + 4 * c;
-          const PageScale page{ps[0], ps[1], ps[2] != 0.0f};
-          const bool ragged = i * 64 + 63 > all_see || i * 64 + 64 > rel_limit || __any(!page.there);
-          weigh(s, page, ragged, i * 64 + 16 * c, rel_limit, row_scale, sees, m, l, o, w0, w1);
-        }
-        lds_barrier();
-        if (active) {
-          const uint8_t* const at = value_lds + (i & 1) * kHalf;
-          const auto fragment = [&](int j) {   // half j / kTilesD of the tokens, channel tile j % kTilesD
-            return reinterpret_cast<const half8*>(at + j % kTilesD * 2048)[j / kTilesD * 64 + lane];
-          };
+      BlockScale bs{};
+      const auto read_scale = [&](int i) {
+        const float4_t v = reinterpret_cast<const float4_t*>(scale_lds)[(i & 3) * 4 + c];
+        bs = BlockScale{v[0], v[1], v[2], __float_as_int(v[3])};
+      };
+      // what a wave does beside the products of block i, in pieces
+      constexpr int kPieceCount = 4 * kMine + 6;
+      const auto piece = [&](int i, int p) {
+        const uint32_t ahead = uint32_t(from + i) * 64;
+        if (p < 2 * kMine) write(value_lds + ((i + 1) & 1) * kHalf, raw_v[p / 2], p / 2, p % 2);
+        else if (p < 4 * kMine) write(key_lds + (i & 1) * kHalf, raw_k[p / 2 - kMine], p / 2 - kMine, p % 2);
+        else if (p == 4 * kMine) write_scale(i + 2);
+        else if (p == 4 * kMine + 1) load_values(ahead + 128, idv);
+        else if (p == 4 * kMine + 2) load_keys(ahead + 192, idk);
+        else if (p == 4 * kMine + 3) raw_page = scale_of(pages, ids, ahead + 192, off_v);
+        else if (p == 4 * kMine + 4) idv = pages.find(ahead + 192, off_v), idk = pages.find(ahead + 256, off_k);
+        else ids = pages.find(ahead + 256, off_v), read_scale(i + 1);
+      };
+      read_scale(0);
+      if (active) {
+        for (int i = 0; i < count; ++i) {
+          const int some = __builtin_amdgcn_readfirstlane(bs.bits);
+          const bool ragged = i * 64 + 63 > all_see || i * 64 + 64 > rel_limit || (some & 4);
+          float mul[RT];
+          half8 w0[RT], w1[RT];
+          refer(s, bs, ragged, i * 64 + 16 * c, rel_limit, row_scale, sees, m, l, o, mul);
+          if (ragged) weigh<true>(s, bs, mul, m, l, w0, w1);
+          else weigh<false>(s, bs, mul, m, l, w0, w1);
+          if (some & 8) drop_zero_values(bs, w0, w1);
+          lds_barrier();
+          __builtin_amdgcn_s_setprio(1);
+          // both products as one run of matrix instructions, each operand block read kAhead blocks before
+          // its use, and the other work in pieces between them; the compiler keeps this order
+          const uint8_t* const values = value_lds + (i & 1) * kHalf;
+          const uint8_t* const keys = key_lds + ((i + 1) & 1) * kHalf;
           half8 ring[kAhead];
 #pragma unroll
-          for (int j = 0; j < kAhead; ++j) ring[j] = fragment(j);
+          for (int j = 0; j < kAhead; ++j) ring[j] = value_block(values, j);
 #pragma unroll
-          for (int j = 0; j < 2 * kTilesD; ++j) {
-            const half8 v = ring[j % kAhead];
-            if (j + kAhead < 2 * kTilesD) ring[j % kAhead] = fragment(j + kAhead);
+          for (int j = 0; j < 2 * kReads; ++j) {
+            const half8 operand = ring[j % kAhead];
+            if (j < kReads) {
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-              o[j % kTilesD][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, j < kTilesD ? w0[rt] : w1[rt],
-                                                                         o[j % kTilesD][rt], 0, 0, 0);
+              for (int rt = 0; rt < RT; ++rt)
+                o[j % kTilesD][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand, j < kTilesD ? w0[rt] : w1[rt],
+                                                                           o[j % kTilesD][rt], 0, 0, 0);
+            } else {
+              score_step(operand, j - kReads);
+            }
+            if (j + kAhead < kReads) ring[j % kAhead] = value_block(values, j + kAhead);
+            else if (j + kAhead < 2 * kReads) ring[j % kAhead] = key_block(keys, j + kAhead - kReads);
+#pragma unroll
+            for (int p = 0; p < kPieceCount; ++p)
+              if (p * 2 * kReads / kPieceCount == j) piece(i, p);
+            __builtin_amdgcn_sched_barrier(0);
           }
-          keep_reads_ahead<2 * kTilesD, RT>();
-          scores(i + 1);
+          __builtin_amdgcn_s_setprio(0);
+          lds_barrier();
         }
-        write(value_lds + ((i + 1) & 1) * kHalf, raw_v);
-        write(key_lds + (i & 1) * kHalf, raw_k);
-        write_scale(i + 2);
-        const uint32_t ahead = uint32_t(from + i) * 64;
-        load_values(ahead + 128, idv);
-        load_keys(ahead + 192, idk);
-        raw_page = scale_of(pages, ids, ahead + 192, off_v);
-        idv = pages.find(ahead + 192, off_v);
-        idk = pages.find(ahead + 256, off_k);
-        ids = pages.find(ahead + 256, off_v);
-        lds_barrier();
+      } else {                                               // a loop of its own: see few_rows_kernel's step
+        for (int i = 0; i < count; ++i) {
+          lds_barrier();
+#pragma unroll
+          for (int p = 0; p < kPieceCount; ++p) piece(i, p);
+          lds_barrier();
+        }
       }
       if (wave < 4) lds_barrier();
     }
@@ -951,10 +1005,11 @@ __global__ __launch_bounds__(256) void join_splits_kernel(Kv8Batch batch, int Hq
 #pragma unroll 4
     for (int s = first; s < splits; s += WAVES) {
       const float2 st = stats[s * rows + row];
-      const float f = st.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(st.x - top);
+      if (st.y == 0.0f) continue;                             // nothing seen there, nothing written
+      const float f = __builtin_amdgcn_exp2f(st.x - top);
       const float4_t p = *reinterpret_cast<const float4_t*>(partial + (s * rows + row) * D + d);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = st.y == 0.0f ? v[i] : __builtin_fmaf(p[i], f, v[i]);
+      for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(p[i], f, v[i]);
     }
   }
   if constexpr (WAVES > 1) {
@@ -1000,11 +1055,10 @@ hipError_t run_attention(const AttentionArgs& a, const Kv8Batch& b, const Kv8Cac
                          hipStream_t stream) {
   constexpr int RT = DT == 256 ? 1 : 2;
   const int64_t groups = b.B * c.H * p.row_blocks * p.splits;
-  if (p.row_tiles == 1)
-    return run_kernel(few_rows_kernel<TIn, DT, 1>, groups, 256, few_rows_lds_bytes<DT, 1>(), a, b, c, stream);
-  if constexpr (DT < 256)
-    if (p.row_tiles == 2)
-      return run_kernel(few_rows_kernel<TIn, DT, 2>, groups, 256, few_rows_lds_bytes<DT, 2>(), a, b, c, stream);
+  constexpr size_t kFew = few_rows_lds_bytes<DT>();
+  if (p.row_tiles == 1) return run_kernel(few_rows_kernel<TIn, DT, 1>, groups, 256, kFew, a, b, c, stream);
+  if (p.row_tiles == 2) return run_kernel(few_rows_kernel<TIn, DT, 2>, groups, 256, kFew, a, b, c, stream);
+  if (p.row_tiles == 4) return run_kernel(few_rows_kernel<TIn, DT, 4>, groups, 256, kFew, a, b, c, stream);
   return run_kernel(many_rows_kernel<TIn, DT, RT>, groups, 512, many_rows_lds_bytes<DT>(), a, b, c, stream);
 }
 
@@ -1045,14 +1099,19 @@ Kv8Plan plan_kv8_attention(int64_t B, int64_t T, int64_t Hq, int64_t H, int64_t 
                            int64_t max_len) {
   Kv8Plan p{};
   const int64_t rows = std::max<int64_t>(std::min(max_new, T), 1) * (Hq / H);
-  const bool many = rows > (D > 128 ? 16 : 32);
-  p.row_tiles = rows <= 16 ? 1 : !many ? 2 : D > 128 ? 8 : 16;
+  const bool many = rows > 64;
+  p.row_tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : !many ? 4 : D > 128 ? 8 : 16;
   p.row_blocks = ceil_div(rows, 16 * p.row_tiles);
-  // tokens are split while there are too few workgroups to fill the chip: about three a compute
-  // unit for few rows, one for many, and at least four blocks of 64 tokens for each (wave)
   const int64_t groups = B * H * p.row_blocks;
-  const int64_t most = std::max<int64_t>(1, max_len / 256);
-  p.splits = int(std::min<int64_t>(std::max<int64_t>(1, (many ? 256 : 768) / groups), std::min<int64_t>(most, 256)));
+  const int64_t blocks = std::max<int64_t>(1, ceil_div(max_len, 64));
+  // Tokens are split where the groups alone do not fill the chip: into about the workgroups that it
+  // holds at once (two a compute unit, one for heads of more than 128 or for many rows), since each
+  // one costs some 5 us to start and to end, and joining costs another 4: 200000 tokens of 8 heads
+  // take 86 us with 512 workgroups and 112 with 1536.  No split has fewer than 8 blocks of 64 tokens
+  // (300 tokens of 16 heads: 7.4 us in one, 10.4 in two).
+  const int64_t hold = many || D > 128 ? 256 : 512;
+  const int64_t wish = many ? hold / groups : ceil_div(hold, groups);
+  p.splits = int(std::min<int64_t>(std::max<int64_t>(1, wish), std::min<int64_t>(std::max<int64_t>(1, blocks / 8), 256)));
   if (p.splits > 1)
     p.bytes = round256(size_t(p.splits) * T * Hq * D * 4) + round256(size_t(p.splits) * T * Hq * 8);
   return p;
