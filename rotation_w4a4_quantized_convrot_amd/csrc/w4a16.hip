@@ -141,11 +141,11 @@ __device__ __forceinline__ void multiply(uint4_t codes, const float (&scale)[4 /
 constexpr int kWaves = 8;
 
 // The end of a workgroup: the waves' sums over their parts of K are added in wave order, then
-// bias and rounding; with partial != NULL the fp32 sums go there instead.
+// bias and rounding.
 template <int ROWS, int COLS, int PARTS>
 __device__ __forceinline__ void finish(const float (*red)[ROWS * COLS], int64_t m0, int64_t n0, int64_t M,
                                        int64_t N, const uint16_t* __restrict__ bias,
-                                       uint16_t* __restrict__ y, float* __restrict__ partial) {
+                                       uint16_t* __restrict__ y) {
   __syncthreads();
   for (int i = threadIdx.x; i < ROWS * COLS; i += kWaves * 64) {
     const int64_t m = m0 + i / COLS, n = n0 + i % COLS;
@@ -153,12 +153,8 @@ __device__ __forceinline__ void finish(const float (*red)[ROWS * COLS], int64_t 
     float s = 0.0f;
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) s += red[p][i];
-    if (partial != nullptr) {
-      partial[m * N + n] = s;
-    } else {
-      if (bias != nullptr) s += bf16_to_f32(bias[n]);
-      y[m * N + n] = f32_to_bf16(s);
-    }
+    if (bias != nullptr) s += bf16_to_f32(bias[n]);
+    y[m * N + n] = f32_to_bf16(s);
   }
 }
 
@@ -171,16 +167,14 @@ __device__ __forceinline__ void finish(const float (*red)[ROWS * COLS], int64_t 
 template <int MB, bool FOLD, int NT, int GC>
 __global__ __launch_bounds__(kWaves * 64) void product_kernel(
     Weights w, const _Float16* __restrict__ op, const float* __restrict__ factor, int64_t rows_padded,
-    int64_t M, int64_t units, const uint16_t* __restrict__ bias, uint16_t* __restrict__ y,
-    float* __restrict__ partial) {
+    int64_t M, int64_t units, const uint16_t* __restrict__ bias, uint16_t* __restrict__ y) {
   constexpr int kHalves = FOLD ? 1 : 2;
   constexpr int kTile = FOLD ? 8 : 16, kRows = FOLD ? 8 : 16 * MB;
   __shared__ float red[FOLD ? 2 * kWaves : kWaves][kRows * kTile * NT];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n = lane & 15, c = lane >> 4;
-  const int64_t n0 = int64_t(blockIdx.x) * (kTile * NT), m0 = int64_t(blockIdx.z) * kRows;
-  const int64_t slices = int64_t(gridDim.y) * kWaves, slice = int64_t(blockIdx.y) * kWaves + wave;
-  const int64_t first = slice * units / slices, last = (slice + 1) * units / slices;
+  const int64_t n0 = int64_t(blockIdx.x) * (kTile * NT), m0 = int64_t(blockIdx.y) * kRows;
+  const int64_t first = wave * units / kWaves, last = (wave + 1) * units / kWaves;
 
   float4_t acc[NT][MB] = {};
   int64_t row[NT];
@@ -204,7 +198,7 @@ __global__ __launch_bounds__(kWaves * 64) void product_kernel(
       }
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
-      const int64_t tile = int64_t(blockIdx.z) * MB + mb;
+      const int64_t tile = int64_t(blockIdx.y) * MB + mb;
 #pragma unroll
       for (int h = 0; h < kHalves; ++h)
 #pragma unroll
@@ -240,20 +234,7 @@ __global__ __launch_bounds__(kWaves * 64) void product_kernel(
           red[wave][(16 * mb + 4 * c + r) * (kTile * NT) + kTile * t + n] = acc[t][mb][r];
         }
       }
-  finish<kRows, kTile * NT, FOLD ? 2 * kWaves : kWaves>(
-      red, m0, n0, M, w.N, bias, y, partial == nullptr ? nullptr : partial + int64_t(blockIdx.y) * M * w.N);
-}
-
-// Adds the sums that workgroups over different parts of K left, in their order.
-__global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ partial, int parts, int64_t M,
-                                                   int64_t N, const uint16_t* __restrict__ bias,
-                                                   uint16_t* __restrict__ y) {
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x, total = M * N;
-  if (i >= total) return;
-  float s = 0.0f;
-  for (int p = 0; p < parts; ++p) s += partial[p * total + i];
-  if (bias != nullptr) s += bf16_to_f32(bias[i % N]);
-  y[i] = f32_to_bf16(s);
+  finish<kRows, kTile * NT, FOLD ? 2 * kWaves : kWaves>(red, m0, n0, M, w.N, bias, y);
 }
 
 // One launch for one or two rows: every wave rotates the activations of its own part of K into
@@ -344,7 +325,7 @@ __global__ __launch_bounds__(kWaves * 64) void vector_kernel(Weights w, const TI
       const int m = (4 * c + r) & 7;
       if (half == (c >> 1) && m < kRows) red[2 * wave + half][m * (8 * NT) + 8 * t + (n & 7)] = acc[t][r];
     }
-  finish<kRows, 8 * NT, 2 * kWaves>(red, 0, n0, M, w.N, bias, y, nullptr);
+  finish<kRows, 8 * NT, 2 * kWaves>(red, 0, n0, M, w.N, bias, y);
 }
 
 // Weights, offline: rotate, one scale bf16(max / 7) per group, codes clamp(rne(value / scale)).
@@ -382,14 +363,14 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 template <int MB, bool FOLD, int NT>
 hipError_t run_product(const Weights& w, int sg, const _Float16* op, const float* factor,
-                       const W4A16Plan& p, int64_t M, const uint16_t* bias, uint16_t* y, float* partial,
+                       const W4A16Plan& p, int64_t M, const uint16_t* bias, uint16_t* y,
                        hipStream_t stream) {
   const int tile = (FOLD ? 8 : 16) * NT, rows = FOLD ? 8 : 16 * MB;
-  const dim3 grid(unsigned(ceil_div(w.N, tile)), unsigned(p.parts), unsigned(ceil_div(M, rows)));
+  const dim3 grid(unsigned(ceil_div(w.N, tile)), unsigned(ceil_div(M, rows)));
   auto kernel = sg == 32 ? product_kernel<MB, FOLD, NT, 1>
                 : sg == 64 ? product_kernel<MB, FOLD, NT, 2> : product_kernel<MB, FOLD, NT, 4>;
   return launch_kernel(kernel, grid, dim3(kWaves * 64), 0, stream, w, op, factor, p.rows_padded, M, p.units,
-                       bias, y, p.parts > 1 ? partial : nullptr);
+                       bias, y);
 }
 
 template <typename TIn, int NT>
@@ -410,30 +391,25 @@ hipError_t run_linear(const TIn* x, int64_t M, int64_t K, int64_t ldx, int g, in
     return run_vector<TIn, 2>(w, sg, x, M, K, ldx, wide, g, p, bias, y, stream);
   _Float16* op = reinterpret_cast<_Float16*>(workspace);
   float* factor = reinterpret_cast<float*>(workspace + p.operand_bytes);
-  float* partial = reinterpret_cast<float*>(workspace + p.operand_bytes + p.factor_bytes);
   const bool fold = M <= 8;
   const int64_t jobs = M * ceil_div(p.units, 4);
-  hipError_t e = launch_kernel(fold ? prepare_kernel<TIn, true> : prepare_kernel<TIn, false>,
+  const hipError_t e = launch_kernel(fold ? prepare_kernel<TIn, true> : prepare_kernel<TIn, false>,
                                dim3(unsigned(ceil_div(jobs, 4))), dim3(256), 0, stream, x, M, K, ldx, wide,
                                digits_of(g), p.units, p.rows_padded, op, factor);
   if (e != hipSuccess) return e;
-  if (fold) e = run_product<1, true, 2>(w, sg, op, factor, p, M, bias, y, partial, stream);
-  else if (M <= 16) e = run_product<1, false, 2>(w, sg, op, factor, p, M, bias, y, partial, stream);
-  else if (M <= 32) e = run_product<2, false, 2>(w, sg, op, factor, p, M, bias, y, partial, stream);
-  else e = run_product<4, false, 2>(w, sg, op, factor, p, M, bias, y, partial, stream);
-  if (e != hipSuccess || p.parts == 1) return e;
-  return launch_kernel(join_kernel, dim3(unsigned(ceil_div(M * w.N, 256))), dim3(256), 0, stream, partial,
-                       p.parts, M, w.N, bias, y);
+  if (fold) return run_product<1, true, 2>(w, sg, op, factor, p, M, bias, y, stream);
+  if (M <= 16) return run_product<1, false, 2>(w, sg, op, factor, p, M, bias, y, stream);
+  if (M <= 32) return run_product<2, false, 2>(w, sg, op, factor, p, M, bias, y, stream);
+  return run_product<4, false, 2>(w, sg, op, factor, p, M, bias, y, stream);
 }
 
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 
 }  // namespace
 
-W4A16Plan plan_w4a16(int64_t M, int64_t N, int64_t Kp) {
+W4A16Plan plan_w4a16(int64_t M, int64_t Kp) {
   W4A16Plan p{};
   p.units = ceil_div(Kp, kUnit);
-  p.parts = 1;
   if (M <= 2) return p;   // the single launch: no workspace
   p.rows_padded = M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : ceil_div(M, 64) * 64;
   p.operand_bytes = round256(size_t(p.rows_padded) * p.units * kUnit * 2);
@@ -444,7 +420,7 @@ W4A16Plan plan_w4a16(int64_t M, int64_t N, int64_t Kp) {
 hipError_t launch_w4a16_linear(const void* x, int x_dtype, int64_t M, int64_t K, int64_t ldx, int g, int sg,
                                int64_t Kp, const uint8_t* wq, const uint16_t* ws, int64_t N,
                                const uint16_t* bias, uint16_t* y, void* workspace, hipStream_t stream) {
-  const W4A16Plan p = plan_w4a16(M, N, Kp);
+  const W4A16Plan p = plan_w4a16(M, Kp);
   const Weights w{wq, ws, N, Kp / 2, Kp / sg};
   uint8_t* work = static_cast<uint8_t*>(workspace);
   if (x_dtype == 0)
