@@ -355,7 +355,8 @@ CONVROT_API int convrot_w4a4_linear_noalloc(const void* x, int32_t x_dtype, int6
 CONVROT_API int64_t convrot_w4a16_padded_k(int64_t K, int64_t g, int64_t sg);
 
 /* Offline weight path: w [N][K] (row stride K) -> wq uint8 [N][K'/2] (16-byte aligned), ws bf16
- * [N][K'/sg] (2-byte aligned).  N = 0 is a no-op.  K' <= CONVROT_MAX_KP.
+ * [N][K'/sg] (2-byte aligned).  N = 0 is a no-op.  K' <= CONVROT_MAX_KP; more rows than a launch
+ * takes (N ceil(K'/1024) > 67108860) are UNSUPPORTED.
  * Errors: GROUP, UNSUPPORTED, SHAPE, NULL, DTYPE, ALIGN, HIP. */
 CONVROT_API int convrot_quant_weight_g4(const void* w, int32_t w_dtype, int64_t N, int64_t K, int64_t g,
                                         int64_t sg, uint8_t* wq, void* ws, void* stream);
@@ -366,8 +367,8 @@ CONVROT_API size_t convrot_w4a16_workspace_bytes(int64_t M, int64_t N, int64_t K
 
 /* The layer: x [M][ldx], ldx >= K (any alignment of the element type), y bf16 [M][N] (2-byte
  * aligned), bias bf16 [N] or NULL.  Made for M up to some 64 rows; more run too, 64 at a time
- * (M <= 4194240).  workspace 256-byte aligned, NULL where it needs 0 bytes.  M = 0 or N = 0 is a
- * no-op.  Results do not depend on the run; rows do not depend on one another.
+ * (M <= 4194240, M ceil(K'/1024) <= 67108860, N <= 134217712).  workspace 256-byte aligned, NULL
+ * where it needs 0 bytes.  M = 0 or N = 0 is a no-op.  Results do not depend on the run; rows do not depend on one another.
  * Errors: GROUP, UNSUPPORTED, SHAPE, NULL, DTYPE, ALIGN, WORKSPACE, HIP. */
 CONVROT_API int convrot_w4a16_linear(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx,
                                      int64_t g, int64_t sg, const uint8_t* wq, const void* ws, int64_t N,
@@ -399,7 +400,7 @@ CONVROT_API int convrot_rotary_frequencies(int64_t R, double base, int32_t scali
  * Outputs may be the inputs themselves (the same pointer and strides), but not overlap them
  * otherwise.  Hk = 0 or Hq = 0: no such tensor (its pointers may be NULL).  dtype of all four.
  * inv_freq fp32 [R/2], pos int64 [T].  T = 0 is a no-op.  R even, 2 <= R <= D <= 1024; at most 65535
- * heads.  Errors: DTYPE, SHAPE, UNSUPPORTED, NULL, ALIGN, HIP. */
+ * heads and 16777215 tokens.  Errors: DTYPE, SHAPE, UNSUPPORTED, NULL, ALIGN, HIP. */
 CONVROT_API int convrot_rotary(const void* q, int64_t q_t, int64_t q_h, void* q_out, int64_t qo_t, int64_t qo_h,
                                int64_t Hq, const void* k, int64_t k_t, int64_t k_h, void* k_out, int64_t ko_t,
                                int64_t ko_h, int64_t Hk, int32_t dtype, int64_t T, int64_t D, int64_t R,
@@ -410,17 +411,19 @@ CONVROT_API int convrot_rotary(const void* q, int64_t q_t, int64_t q_h, void* q_
  *   kc int8 [num_pages][H][page][D], ks fp32 [num_pages][H]: key = code * scale, rotated in windows
  *   of g (0: not; else 16, 64 or 256, a divisor of D) by H_g / sqrt(g);
  *   vc int8 [num_pages][H][D][page], vs fp32 [num_pages][H]: value = code * scale (not rotated).
- * D a multiple of 16, at most 256.  kc, vc 16-byte aligned.
+ * D a multiple of 16, at most 256.  kc, vc 16-byte aligned.  B H at most 8388607.
  *
  * A batch is described on the DEVICE, by the same three int32 arrays for every call of a step:
  *   cu [B+1]      the rows of sequence b among the call's T rows are cu[b] ... cu[b+1]-1;
  *   lens [B]      its length, those rows included: they are its last tokens;
  *   table [B][max_pages] (row stride table_ld): its pages in order.
- * What does not fit is skipped, never followed: sequences whose rows are not within [0, T], table
- * entries outside [0, num_pages), tokens beyond max_pages pages.  max_new and max_len are the largest
+ * What does not fit is skipped, never followed: sequences whose rows are not within [0, T] (these rows
+ * are then of no sequence), table entries outside [0, num_pages), tokens beyond max_pages pages; append
+ * and read skip a sequence that has more rows than its length, and to attention its first rows
+ * see nothing.  max_new and max_len are the largest
  * row count and length the caller expects; they only size the launch, and larger ones are right
- * too.  A page that receives rows must belong to one sequence; pages that are only read may be
- * shared. */
+ * too.  A page that receives rows must belong to one sequence and stand in its table once, and two
+ * calls that write it must follow one another; pages that are only read may be shared. */
 
 /* Writes rows k, v [T][H][D] (strides in elements) into the cache.  The scale of a page covers its
  * tokens: S = fp32(max |value| / 127) of the new rows, or the page's scale if tokens of this sequence
@@ -457,7 +460,8 @@ CONVROT_API size_t convrot_kv8_attention_workspace_bytes(int64_t T, int64_t B, i
  * is zero; rows of no sequence are left as they were; a row whose q holds an Inf or a NaN, or that sees a
  * page with a NaN scale, is NaN.  Scales are 0 or at least 2^-80, as append writes them.
  * Results do not depend on the run.  workspace 256-byte aligned, NULL where it needs 0 bytes; T, B, Hq, H,
- * D, max_new and max_len as given to the workspace function.
+ * D, max_new and max_len as given to the workspace function.  T Hq below 2^31, below 2^24 where the tokens
+ * are split (UNSUPPORTED otherwise).
  * Errors: GROUP, UNSUPPORTED, SHAPE, NULL, DTYPE, ALIGN, WORKSPACE, HIP. */
 CONVROT_API int convrot_kv8_attention(const void* q, int64_t q_t, int64_t q_h, int32_t dtype, int64_t T,
                                       int64_t Hq, const int32_t* cu, const int32_t* lens,

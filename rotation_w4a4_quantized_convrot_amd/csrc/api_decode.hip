@@ -8,6 +8,9 @@
 namespace {
 
 constexpr int64_t kIntMax = 0x7FFFFFFF;
+// A launch takes fewer than 2^32 threads along x; what would need more is refused here, before it
+// becomes an error that the runtime keeps for a later call to find.
+constexpr int64_t kMaxThreads = 0xFFFFFFFF;
 constexpr int64_t kMaxStride = int64_t(1) << 46;   // elements; keeps every offset within 63 bits
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -22,6 +25,8 @@ int check_window(int64_t g, int64_t most) {
   return g >= 16 && g <= most ? CONVROT_OK : CONVROT_ERR_UNSUPPORTED;
 }
 
+bool launch_fits(int64_t workgroups, int64_t threads) { return workgroups <= kMaxThreads / threads; }
+
 int check_w4a16(int64_t M, int64_t N, int64_t K, int64_t g, int64_t sg, int64_t* kp) {
   const int st = check_window(g, 1024);
   if (st != CONVROT_OK) return st;
@@ -29,6 +34,9 @@ int check_w4a16(int64_t M, int64_t N, int64_t K, int64_t g, int64_t sg, int64_t*
   if (*kp < 0) return int(*kp);
   if (M < 0 || N < 0 || M > kIntMax || N > kIntMax) return CONVROT_ERR_SHAPE;
   if (*kp > CONVROT_MAX_KP || M > 65535 * int64_t(64)) return CONVROT_ERR_UNSUPPORTED;
+  // workgroups of at least 16 weight rows and 512 threads; preparing x takes a wave for 1024 columns
+  if (!launch_fits((N + 15) / 16, 512) || !launch_fits((M * ((*kp + 1023) / 1024) + 3) / 4, 256))
+    return CONVROT_ERR_UNSUPPORTED;
   return CONVROT_OK;
 }
 
@@ -41,7 +49,7 @@ int check_cache(int64_t num_pages, int64_t page, int64_t H, int64_t D, int64_t g
     return CONVROT_ERR_SHAPE;
   if (page != 16 && page != 32 && page != 64 && page != 128) return CONVROT_ERR_UNSUPPORTED;
   if (D % 16 != 0 || D > 256 || (g != 0 && D % g != 0)) return CONVROT_ERR_UNSUPPORTED;
-  if (H > 65535 || B > kIntMax / (2 * H)) return CONVROT_ERR_UNSUPPORTED;
+  if (H > 65535 || B > kMaxThreads / 256 / (2 * H)) return CONVROT_ERR_UNSUPPORTED;
   return CONVROT_OK;
 }
 
@@ -59,6 +67,11 @@ int check_batch_pointers(const int32_t* cu, const int32_t* lens, const int32_t* 
 bool attention_shape_ok(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t max_new, int64_t max_len) {
   return T >= 0 && T <= kIntMax && B >= 0 && B <= kIntMax && H >= 1 && H <= 65535 && Hq >= 1 && Hq <= 65535 &&
          Hq % H == 0 && D >= 1 && max_new >= 0 && max_len >= 0 && max_new <= kIntMax && max_len <= kIntMax;
+}
+
+// Within these the plan's counts stay far inside 64 bits.
+bool attention_plannable(int64_t T, int64_t B, int64_t Hq, int64_t H) {
+  return T <= kIntMax / Hq && B <= kMaxThreads / 256 / (2 * H);
 }
 
 }  // namespace
@@ -79,6 +92,7 @@ int convrot_quant_weight_g4(const void* w, int32_t w_dtype, int64_t N, int64_t K
   int64_t kp = 0;
   const int st = check_w4a16(0, N, K, g, sg, &kp);
   if (st != CONVROT_OK) return st;
+  if (!launch_fits((N * ((kp + 1023) / 1024) + 3) / 4, 256)) return CONVROT_ERR_UNSUPPORTED;
   if (elem_size(w_dtype) == 0) return CONVROT_ERR_DTYPE;
   if (N == 0) return CONVROT_OK;
   if (w == nullptr || wq == nullptr || ws == nullptr) return CONVROT_ERR_NULL;
@@ -149,7 +163,7 @@ int convrot_rotary(const void* q, int64_t q_t, int64_t q_h, void* q_out, int64_t
   const size_t size = elem_size(dtype);
   if (size == 0) return CONVROT_ERR_DTYPE;
   if (T < 0 || T > kIntMax || Hq < 0 || Hk < 0 || D < 1 || R < 2 || R % 2 != 0 || R > D) return CONVROT_ERR_SHAPE;
-  if (D > 1024 || Hq > 65535 || Hk > 65535 - Hq) return CONVROT_ERR_UNSUPPORTED;
+  if (D > 1024 || Hq > 65535 || Hk > 65535 - Hq || !launch_fits(T, 256)) return CONVROT_ERR_UNSUPPORTED;
   const struct {
     const void* in;
     int64_t in_t, in_h;
@@ -221,7 +235,9 @@ int convrot_kv8_read(const int32_t* cu, const int32_t* lens, const int32_t* tabl
 
 size_t convrot_kv8_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D,
                                              int64_t max_new, int64_t max_len) {
-  if (!attention_shape_ok(T, B, Hq, H, D, max_new, max_len) || T == 0 || B == 0 || D > 256 || D % 16 != 0) return 0;
+  if (!attention_shape_ok(T, B, Hq, H, D, max_new, max_len) || !attention_plannable(T, B, Hq, H) || T == 0 ||
+      B == 0 || D > 256 || D % 16 != 0)
+    return 0;
   return convrot::plan_kv8_attention(B, T, Hq, H, D, max_new, max_len).bytes;
 }
 
@@ -237,8 +253,12 @@ int convrot_kv8_attention(const void* q, int64_t q_t, int64_t q_h, int32_t dtype
   if (!attention_shape_ok(T, B, Hq, H, D, max_new, max_len) || !stride_ok(q_t) || !stride_ok(q_h))
     return CONVROT_ERR_SHAPE;
   if (T == 0 || B == 0) return CONVROT_OK;
+  if (!attention_plannable(T, B, Hq, H)) return CONVROT_ERR_UNSUPPORTED;
   const convrot::Kv8Plan plan = convrot::plan_kv8_attention(B, T, Hq, H, D, max_new, max_len);
-  if (plan.row_blocks > kIntMax / plan.splits / H / B || T > kIntMax / Hq) return CONVROT_ERR_UNSUPPORTED;
+  // workgroups of 256 threads for few rows, 512 for many; joining the splits takes one to a row at most
+  if (plan.row_blocks > kMaxThreads / (plan.row_tiles <= 4 ? 256 : 512) / plan.splits / H / B ||
+      (plan.splits > 1 && !launch_fits(T * Hq, 256)))
+    return CONVROT_ERR_UNSUPPORTED;
   if (q == nullptr || out == nullptr || (plan.bytes > 0 && workspace == nullptr)) return CONVROT_ERR_NULL;
   st = check_batch_pointers(cu, lens, table, max_pages, kc, ks, vc, vs);
   if (st != CONVROT_OK) return st;

@@ -233,3 +233,30 @@ def test_binding_checks_cache():
             match="heads")
     _raises(cr.ConvAttention, cr.ConvLinearW4A16(64, 96, 16, 32), cr.ConvLinearW4A16(64, 64, 16, 32), 4, 2, z((6,), f32),
             match="features|multiple")
+
+
+def test_sizes_past_a_launch_are_refused(lib):
+    """What would need 2^32 threads along a grid's axis, or counts past 64 bits, never reaches a launch."""
+    linear = lambda M, N, K: lib.convrot_w4a16_linear(A, 1, M, K, K, 16, 32, A, A, N, None, A, None, 0, None)  # noqa: E731
+    assert linear(1, 134217713, 64) == linear(4000000, 4, 65536) == E.CONVROT_ERR_UNSUPPORTED
+    assert cr.convrot_w4a16_workspace_bytes(4000000, 4, 65536, 16, 32) == 0
+    assert cr.convrot_w4a16_workspace_bytes(4000000, 4, 4096, 16, 32) >= 4000000 * 4096 * 2
+    assert linear(3, 134217712, 64) == E.CONVROT_ERR_NULL                # the limit itself: asks for its workspace
+    quant = lambda N, K: lib.convrot_quant_weight_g4(None, 1, N, K, 16, 32, A, A, None)  # noqa: E731
+    assert quant(67108861, 64) == quant(2 ** 31 - 1, 65536) == E.CONVROT_ERR_UNSUPPORTED
+    assert quant(67108860, 64) == E.CONVROT_ERR_NULL
+    rotary = lambda T: lib.convrot_rotary(None, 64, 64, None, 64, 64, 1, None, 0, 0, None, 0, 0, 0, 1, T, 64, 32, A, A,  # noqa: E731
+                                          0, ctypes.c_float(1.0), 0, None)
+    assert rotary(2 ** 24) == E.CONVROT_ERR_UNSUPPORTED and rotary(2 ** 24 - 1) == E.CONVROT_ERR_NULL
+    append = lambda B: lib.convrot_kv8_append(None, 64, 64, None, 64, 64, 1, 5, A, A, A, 4, B, 4, A, A, A, A, 10, 16, 1,  # noqa: E731
+                                              64, 16, 1, None)
+    assert append(8388608) == E.CONVROT_ERR_UNSUPPORTED and append(8388607) == E.CONVROT_ERR_NULL
+    attend = lambda T, Hq, B, new, ln: lib.convrot_kv8_attention(  # noqa: E731
+        None, 64, 64, 1, T, Hq, A, A, A, 4, B, 4, A, A, A, A, 10, 16, 1, 64, 16, ctypes.c_float(0.1), new, ln, A, A, 1 << 60,
+        None)
+    assert attend(2 ** 24, 1, 1, 1, 100000) == E.CONVROT_ERR_UNSUPPORTED     # its tokens are split: a join of 2^24 rows
+    assert attend(2 ** 24 - 1, 1, 1, 1, 100000) == attend(2 ** 24, 1, 1, 1, 100) == E.CONVROT_ERR_NULL
+    assert attend(2 ** 24, 128, 1, 1, 100) == attend(2 ** 20, 64, 4000, 2 ** 20, 100) == E.CONVROT_ERR_UNSUPPORTED
+    nbytes = cr.convrot_kv8_attention_workspace_bytes
+    assert nbytes(2 ** 27, 2 ** 30, 2 ** 15, 2 ** 15, 128, 2 ** 27, 1000) == 0      # 2^64 workgroups
+    assert nbytes(2 ** 31 - 1, 2 ** 22, 2 ** 15, 1, 256, 2 ** 31 - 1, 2 ** 31 - 1) == 0
