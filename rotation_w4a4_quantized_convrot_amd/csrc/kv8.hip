@@ -793,7 +793,7 @@ __global__ __launch_bounds__(512) void many_rows_kernel(AttentionArgs a, Kv8Batc
     const bool active = r0 < w.rows;                               // the wave has rows
     // tokens that any row of the workgroup sees, in blocks of 64; this split's share of them
     const int64_t limit = min(w.len, w.before + (min(rb * kRows + kRows, w.rows) - 1) / G + 1);
-        const int64_t blocks = limit > 0 ? (limit + 63) / 64 : 0;
+    const int64_t blocks = limit > 0 ? (limit + 63) / 64 : 0;
     const int64_t per = (blocks + a.splits - 1) / a.splits;
     const int64_t from = w.split * per;
     const int count = int(max(min(per, blocks - from), int64_t(0)));
@@ -985,7 +985,12 @@ __global__ __launch_bounds__(256) void join_splits_kernel(Kv8Batch batch, int Hq
   const int64_t row = int64_t(blockIdx.x) * kPerBlock + wave / WAVES;
   if (row >= rows) return;
   const int64_t t = row / Hq;
-  if (t < batch.cu[0] || t >= batch.cu[batch.B]) return;      // a row of no sequence: left as it is
+  bool there = false;
+  for (int64_t i = lane; i < batch.B; i += 64) {
+    const Sequence seq = sequence_of(batch, i);
+    there = there || (t >= seq.row0 && t < seq.row0 + seq.n);
+  }
+  if (!__any(there)) return;                                  // a row of no sequence: left as it is
   float top = kNothing;
   for (int s = lane; s < splits; s += 64) top = fmaxf(top, stats[s * rows + row].x);
 #pragma unroll

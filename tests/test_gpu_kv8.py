@@ -287,6 +287,27 @@ def test_attention_padded_batch_and_empty_rows(cr):
         assert bool((out[9:13] == 0).all()) and bool((out[19] == 0).all()) and bool((ref[9:13] == 0).all())
 
 
+@pytest.mark.parametrize("cu", [[0, 3, 50], [0, 3, 3, 60, 8], [2, 90, 5, 9]])
+@pytest.mark.parametrize("max_len", [100, 4000])             # one split of the tokens, and several
+def test_attention_leaves_rows_of_no_sequence(cr, cu, max_len):
+    """Sequences whose rows are not all among the T rows have none: their rows stay, split or not."""
+    print(f"\n[case] attention rows of no sequence cu={cu} max_len={max_len}", flush=True)
+    gen = torch.Generator().manual_seed(len(cu))
+    Hq, H, D, page, T, B = 4, 2, 64, 16, 12, len(cu) - 1
+    lens = [60] * B
+    table, pages = paging(lens, page, gen)
+    cache = cache_of(pages, H, page, D, gen)
+    q = torch.randn((T, Hq, D), generator=gen).to(torch.bfloat16)
+    cu, ln = torch.tensor(cu, dtype=torch.int32), torch.tensor(lens, dtype=torch.int32)
+    need = cr.convrot_kv8_attention_workspace_bytes(T, B, Hq, H, D, T, max_len)
+    assert (need > 0) == (max_len == 4000)
+    work = torch.full((max(need, 256),), 0x3F, dtype=torch.uint8, device=DEV)     # what an earlier call left
+    out = torch.full((T, Hq, D), 3.0, dtype=torch.bfloat16, device=DEV)
+    cr.convrot_kv8_attention(q.to(DEV), cu.to(DEV), ln.to(DEV), table.to(DEV), *to(cache), out=out, max_len=max_len,
+                             workspace=work)
+    check_attention(out, q, cu, ln, table, cache, 0, 1 / math.sqrt(D), fill=3.0)
+
+
 def test_attention_not_finite_and_zero_scales(cr):
     print("\n[case] attention NaN, Inf, zero scales", flush=True)
     gen = torch.Generator().manual_seed(4)
