@@ -105,7 +105,7 @@ int convrot_quant_weight_g4(const void* w, int32_t w_dtype, int64_t N, int64_t K
 size_t convrot_w4a16_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t g, int64_t sg) {
   int64_t kp = 0;
   if (check_w4a16(M, N, K, g, sg, &kp) != CONVROT_OK || M == 0 || N == 0) return 0;
-  const convrot::W4A16Plan p = convrot::plan_w4a16(M, kp);
+  const convrot::W4A16Plan p = convrot::plan_w4a16(M, kp, int(g));
   return p.operand_bytes + p.factor_bytes;
 }
 

@@ -77,10 +77,11 @@ hipError_t launch_quant_weight_g4(const void* w, int w_dtype, int64_t N, int64_t
 // How the W4A16 product of M rows runs, and the workspace it needs.
 struct W4A16Plan {
   int64_t units;        // of 256 columns of the padded depth
+  int vector_units;     // one or two rows: of a wave, all of its part of K at once (1, 2, 4 or 8); 0: more of them
   int64_t rows_padded;  // activation rows of the prepared operand; 0: one launch, no workspace
   size_t operand_bytes, factor_bytes;
 };
-W4A16Plan plan_w4a16(int64_t M, int64_t Kp);
+W4A16Plan plan_w4a16(int64_t M, int64_t Kp, int g);
 hipError_t launch_w4a16_linear(const void* x, int x_dtype, int64_t M, int64_t K, int64_t ldx, int g, int sg,
                                int64_t Kp, const uint8_t* wq, const uint16_t* ws, int64_t N,
                                const uint16_t* bias, uint16_t* y, void* workspace, hipStream_t stream);

@@ -124,6 +124,16 @@ __device__ __forceinline__ uint32_t row_max(uint32_t m) {
   return max(m, lane_dpp_u<kRowRor8>(m));
 }
 
+// Maximum over a row of 16 lanes, or over the wave where a window of 1024 spans it.
+__device__ __forceinline__ uint32_t unit_max(uint32_t m, int digits) {
+  m = row_max(m);
+  if (digits >= 5) {
+    m = max(m, uint32_t(__shfl_xor(int(m), 16)));
+    m = max(m, uint32_t(__shfl_xor(int(m), 32)));
+  }
+  return m;
+}
+
 // An exact power of two that takes values of largest magnitude `bits`, times `growth` = 2^grow
 // at most, to at most 2^15 (fp16 holds 65504), and its inverse.  A zero row gives 1; a row that
 // holds an Inf or a NaN gives an inverse of NaN, which the caller multiplies the row's result
@@ -137,6 +147,11 @@ __device__ __forceinline__ void half_range(uint32_t bits, int grow, float* to_ha
   *back = bits == 0 ? 1.0f
           : bits >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
                                 : __uint_as_float(uint32_t(127 - up) << 23);
+}
+
+// A barrier for what is in LDS: loads from memory may still be on their way.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 __host__ __device__ __forceinline__ int digits_of(int g) {

@@ -7,6 +7,9 @@
 // Angles of far positions do not fit fp32 (position 10^6 times a frequency near 1 has an error of
 // 0.06 rad there), so each angle is taken in fp64 in turns and only its fraction goes to fp32.
 // A workgroup takes a token: its R/2 cosines and sines go to LDS once, for all of its heads.
+//
+// Every element is read and written once, which bounds it: 16384 tokens of 40 heads of 128 in bf16
+// (336 MB) take 82.8 us, 4.05 TB/s (a large copy: 4.95); 8 tokens 4.2 us, the launch.
 #include "decode_device.h"
 
 #include <algorithm>

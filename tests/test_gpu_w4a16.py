@@ -76,6 +76,21 @@ def test_linear_matches_definition(cr, M, K, N, g, sg, dtype, with_bias):
     assert torch.equal(again.view(torch.int16), y.view(torch.int16).contiguous())
 
 
+@pytest.mark.parametrize("M,K,N,g,sg,dtype", [
+    # more tiles of weight rows than workgroups, one to eight units of K a wave; the longest rows of that kind and
+    # the first that are longer
+    (1, 1030, 9001, 64, 32, "bf16"), (2, 2100, 8200, 0, 128, "f32"), (1, 3800, 5003, 1024, 128, "bf16"),
+    (2, 7000, 4500, 256, 32, "f32"), (1, 12000, 4200, 16, 64, "bf16"), (2, 16384, 70, 1024, 128, "f32"),
+    (1, 16384, 2050, 256, 64, "bf16"), (2, 16385, 40, 64, 128, "bf16"), (1, 100, 8300, 16, 32, "f32"),
+])
+def test_linear_one_or_two_rows(cr, M, K, N, g, sg, dtype):
+    print(f"\n[case] w4a16 rows M={M} K={K} N={N} g={g} sg={sg} {dtype}", flush=True)
+    x, wq, ws, bias = _inputs(M, K, N, g, sg, torch.float32 if dtype == "f32" else torch.bfloat16, K + N, cr)
+    assert cr.convrot_w4a16_workspace_bytes(M, N, K, g, sg) == 0
+    y = cr.convrot_w4a16_linear(*(t.to(DEV) if isinstance(t, torch.Tensor) else t for t in (x, g, sg, wq, ws, bias)))
+    _check(y, x, g, wq, ws, bias)
+
+
 @pytest.mark.parametrize("M,offset,ld", [(1, 1, 1111), (2, 3, 1003), (7, 1, 1001), (20, 5, 1008), (4, 8, 1016)])
 def test_linear_strided_and_unaligned_rows(cr, M, offset, ld):
     print(f"\n[case] w4a16 rows M={M} offset={offset} ld={ld}", flush=True)
