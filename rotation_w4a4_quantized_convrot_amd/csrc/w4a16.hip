@@ -155,6 +155,66 @@ __device__ __forceinline__ void finish(const float (*red)[ROWS * COLS], int64_t 
   }
 }
 
+// Scale groups as the kernels see them: GC loads' 32-code chunks share a scale; WHOLE: rows are whole
+// loads of 128 codes (K' is a multiple of 128), so a load's scales are neighbours in one row.
+template <int GC_, bool WHOLE_>
+struct Groups {
+  static constexpr int GC = GC_;
+  static constexpr bool WHOLE = WHOLE_ || GC_ == 4;
+};
+
+// Eight or sixteen weight rows as a lane sees them: the first row's address is the wave's, the lane's row
+// from there an offset of 32 bits (16 rows of at most 32 KB).  Rows past the last are the last one.
+struct Rows {
+  const uint8_t* codes;
+  const uint16_t* scales;
+  uint32_t row_codes, row_scales;     // offsets of the lane's row, in bytes and in scales
+
+  __device__ __forceinline__ void set(const Weights& w, int64_t first, int lane_row) {
+    const int64_t row = min(first, w.N - 1);
+    codes = w.codes + row * w.row_bytes;
+    scales = w.scales + row * w.groups;
+    const uint32_t r = uint32_t(min(int64_t(lane_row), w.N - 1 - row));
+    row_codes = r * uint32_t(w.row_bytes);
+    row_scales = r * uint32_t(w.groups);
+  }
+};
+
+// One load of a row: 16 bytes of codes (32 of them) at chunk + c, and the 4 / GC scales of the chunks
+// chunk ... chunk + 3.  Past the row's end (the activations are zero there) its first ones.  Nothing is
+// computed from what is loaded before it is used, and it stays where it was loaded to, so that
+// nothing waits for loads that are on their way.
+template <typename G>
+struct Load {
+  uint4_t codes;
+  uint16_t scale[G::WHOLE && G::GC != 4 ? 1 : 4 / G::GC];      // raw bf16, or as loaded together:
+  uint32_t pair[G::WHOLE && G::GC < 4 ? 2 / G::GC : 1];
+
+  __device__ __forceinline__ void from(const Weights& w, const Rows& rows, int chunk, int c) {
+    const uint32_t byte = uint32_t(chunk + c) * 16;
+    codes = *reinterpret_cast<const uint4_t*>(rows.codes + (rows.row_codes + (byte < uint32_t(w.row_bytes) ? byte : 0u)));
+    uint32_t j = uint32_t(chunk) / G::GC;
+    if constexpr (G::WHOLE) {
+      j = rows.row_scales + (j < uint32_t(w.groups) ? j : 0u);
+      if constexpr (G::GC == 4) scale[0] = rows.scales[j];
+      else __builtin_memcpy(pair, rows.scales + j, 8 / G::GC);
+    } else {            // the row may end between them
+#pragma unroll
+      for (int i = 0; i < 4 / G::GC; ++i) scale[i] = rows.scales[rows.row_scales + min(j + i, uint32_t(w.groups - 1))];
+    }
+  }
+
+  __device__ __forceinline__ void scales(float (&out)[4 / G::GC]) const {
+#pragma unroll
+    for (int i = 0; i < 4 / G::GC; ++i) {
+      if constexpr (G::WHOLE && G::GC < 4)
+        out[i] = __uint_as_float(i % 2 ? pair[i / 2] & 0xFFFF0000u : pair[i / 2] << 16);
+      else
+        out[i] = bf16_to_f32(scale[i]);
+    }
+  }
+};
+
 // The product for prepared activations.  A workgroup takes NT tiles of weight rows and 16 * MB
 // (FOLD: 8) activation rows; its eight waves take parts of K, so that each weight line is read by
 // one wave and the activation operand goes straight into registers.  FOLD, for M <= 8: a load
@@ -239,65 +299,70 @@ __global__ __launch_bounds__(kWaves * 64) void product_kernel(
   finish<kRows, kTile * NT, FOLD ? 2 * kWaves : kWaves>(red, m0, n0, M, w.N, bias, y);
 }
 
-// Scale groups as the kernels see them: GC loads' 32-code chunks share a scale; WHOLE: rows are whole
-// loads of 128 codes (K' is a multiple of 128), so a load's scales are neighbours in one row.
-template <int GC_, bool WHOLE_>
-struct Groups {
-  static constexpr int GC = GC_;
-  static constexpr bool WHOLE = WHOLE_ || GC_ == 4;
-};
+// The product for prepared activations where tiles of 32 weight rows are too few for the chip: one tile of
+// 16, the waves' parts of K in steps of one load (128 columns), and what the next step needs asked for as
+// soon as this one has used the same registers.  32 x 12288 to 4096: 21 us with the activations' launch, 32
+// in product_kernel's tiles, which leave half the compute units idle.  Where there are enough of those
+// the operand, read once a tile, decides instead: 64 x 8192 to 28672 takes 128 us so, 80 in tiles of 64 rows.
+template <int MB, typename G>
+__global__ __launch_bounds__(kWaves * 64, 2) void narrow_kernel(Weights w, const _Float16* __restrict__ op,
+                                                                const float* __restrict__ factor,
+                                                                int64_t rows_padded, int64_t M, int64_t units,
+                                                                const uint16_t* __restrict__ bias,
+                                                                uint16_t* __restrict__ y) {
+  constexpr int kRows = 16 * MB;
+  __shared__ float red[kWaves][kRows * 16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, c = lane >> 4;
+  const int64_t n0 = int64_t(blockIdx.x) * 16, m0 = int64_t(blockIdx.y) * kRows;
+  const int steps = int(units) * 2, first = wave * steps / kWaves, last = (wave + 1) * steps / kWaves;
 
-// Eight weight rows as a lane sees them: the first row's address is the wave's, the lane's row from there
-// an offset of 32 bits (8 rows of at most 8 KB).  Rows past the last are the last one.
-struct Rows {
-  const uint8_t* codes;
-  const uint16_t* scales;
-  uint32_t row_codes, row_scales;     // offsets of the lane's row, in bytes and in scales
-
-  __device__ __forceinline__ void set(const Weights& w, int64_t first, int lane_row) {
-    const int64_t row = min(first, w.N - 1);
-    codes = w.codes + row * w.row_bytes;
-    scales = w.scales + row * w.groups;
-    const uint32_t r = uint32_t(min(int64_t(lane_row), w.N - 1 - row));
-    row_codes = r * uint32_t(w.row_bytes);
-    row_scales = r * uint32_t(w.groups);
-  }
-};
-
-// One load of a row: 16 bytes of codes (32 of them) at chunk + c, and the 4 / GC scales of the chunks
-// chunk ... chunk + 3.  Past the row's end (the activations are zero there) its first ones.  Nothing is
-// computed from what is loaded before it is used, and it stays where it was loaded to, so that
-// nothing waits for loads that are on their way.
-template <typename G>
-struct Load {
-  uint4_t codes;
-  uint16_t scale[G::WHOLE && G::GC != 4 ? 1 : 4 / G::GC];      // raw bf16, or as loaded together:
-  uint32_t pair[G::WHOLE && G::GC < 4 ? 2 / G::GC : 1];
-
-  __device__ __forceinline__ void from(const Weights& w, const Rows& rows, int chunk, int c) {
-    const uint32_t byte = uint32_t(chunk + c) * 16;
-    codes = *reinterpret_cast<const uint4_t*>(rows.codes + (rows.row_codes + (byte < uint32_t(w.row_bytes) ? byte : 0u)));
-    uint32_t j = uint32_t(chunk) / G::GC;
-    if constexpr (G::WHOLE) {
-      j = rows.row_scales + (j < uint32_t(w.groups) ? j : 0u);
-      if constexpr (G::GC == 4) scale[0] = rows.scales[j];
-      else __builtin_memcpy(pair, rows.scales + j, 8 / G::GC);
-    } else {            // the row may end between them
+  float4_t acc[MB] = {};
+  Rows rows;
+  rows.set(w, n0, n);
+  Load<G> weights;
+  half8 x[MB][4];
+  float4_t f[MB];
+  const auto load_x = [&](int step) {
+    const int64_t u = step / 2;
 #pragma unroll
-      for (int i = 0; i < 4 / G::GC; ++i) scale[i] = rows.scales[rows.row_scales + min(j + i, uint32_t(w.groups - 1))];
+    for (int mb = 0; mb < MB; ++mb) {
+      const int64_t tile = int64_t(blockIdx.y) * MB + mb;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t block = (tile * units + u) * 8 + (step & 1) * 4 + j;
+        x[mb][j] = *reinterpret_cast<const half8*>(op + (block * 64 + lane) * 8);
+      }
+      f[mb] = *reinterpret_cast<const float4_t*>(factor + u * rows_padded + m0 + 16 * mb + 4 * c);
     }
+  };
+  const auto advance = [&](auto more, int step) {
+    float scale[4 / G::GC];
+    weights.scales(scale);
+    float4_t sum[MB] = {};
+    multiply<MB, G::GC>(weights.codes, scale, x, sum);
+    if constexpr (decltype(more)::value) weights.from(w, rows, (step + 1) * 4, c);
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[mb][r] = __builtin_fmaf(f[mb][r], sum[mb][r], acc[mb][r]);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (decltype(more)::value) load_x(step + 1);
+  };
+  if (first < last) {
+    weights.from(w, rows, first * 4, c);
+    load_x(first);
+    for (int step = first; step + 1 < last; ++step) advance(std::true_type{}, step);
+    advance(std::false_type{}, last - 1);
   }
 
-  __device__ __forceinline__ void scales(float (&out)[4 / G::GC]) const {
 #pragma unroll
-    for (int i = 0; i < 4 / G::GC; ++i) {
-      if constexpr (G::WHOLE && G::GC < 4)
-        out[i] = __uint_as_float(i % 2 ? pair[i / 2] & 0xFFFF0000u : pair[i / 2] << 16);
-      else
-        out[i] = bf16_to_f32(scale[i]);
-    }
-  }
-};
+  for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) red[wave][(16 * mb + 4 * c + r) * 16 + n] = acc[mb][r];
+  __syncthreads();
+  finish<kRows, 16, kWaves>(red, m0, n0, M, w.N, bias, y);
+}
 
 // One launch for one or two rows of up to 64 units.  A wave takes U units of K of every tile that its
 // workgroup goes through (8 NT weight rows, folded as above): it rotates its columns of the activations once,
@@ -306,9 +371,10 @@ struct Load {
 // activation row, four of them at a time (a window of 1024: the four units of one row).
 //
 // The weights' bytes bound it.  1 x 8192 to 28672 (121 MB): 28.5 us, 4.2 TB/s, where a plain read of as
-// much reaches 5.5; 35.7 us with x rotated again for every tile (long_vector_kernel), 40.7 with half the
-// registers and two workgroups a compute unit, which spills the loads.  1 x 4096 to 4096: 6.2 us; 1 x 1024
-// to 1024: 4.6 us, of which the launch is most.
+// much reaches 5.5; 35.7 us with x rotated again for every tile (long_vector_kernel).  One workgroup a
+// compute unit with 256 registers a lane: in an earlier form 35.9 us so and 40.7 with two workgroups of 128
+// registers, which do not hold the loads.  1 x 4096 to 4096: 6.2 us; 1 x 1024 to 1024: 4.6 us, of which the
+// launch is most.
 template <int U>
 __host__ __device__ constexpr size_t vector_lds_bytes(int M) {
   return size_t(kWaves) * M * U * (2 * 136 * 2 + 4);      // a unit's halves 16 bytes apart in the banks
@@ -534,6 +600,25 @@ __global__ __launch_bounds__(256) void quant_weight_kernel(const TIn* __restrict
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Calls `run` with the Groups that a scale group of sg values and rows of row_bytes make.
+template <typename Run>
+hipError_t with_groups(const Weights& w, int sg, Run run) {
+  const bool whole = w.row_bytes % 64 == 0;
+  if (sg == 128) return run(Groups<4, true>{});
+  if (sg == 64) return whole ? run(Groups<2, true>{}) : run(Groups<2, false>{});
+  return whole ? run(Groups<1, true>{}) : run(Groups<1, false>{});
+}
+
+template <int MB>
+hipError_t run_narrow(const Weights& w, int sg, const _Float16* op, const float* factor, const W4A16Plan& p,
+                      int64_t M, const uint16_t* bias, uint16_t* y, hipStream_t stream) {
+  const dim3 grid(unsigned(ceil_div(w.N, 16)), unsigned(ceil_div(M, 16 * MB)));
+  return with_groups(w, sg, [&](auto groups) {
+    return launch_kernel(narrow_kernel<MB, decltype(groups)>, grid, dim3(kWaves * 64), 0, stream, w, op, factor,
+                         p.rows_padded, M, p.units, bias, y);
+  });
+}
+
 template <int MB, bool FOLD, int NT>
 hipError_t run_product(const Weights& w, int sg, const _Float16* op, const float* factor,
                        const W4A16Plan& p, int64_t M, const uint16_t* bias, uint16_t* y,
@@ -546,30 +631,22 @@ hipError_t run_product(const Weights& w, int sg, const _Float16* op, const float
                        bias, y);
 }
 
-template <typename TIn, int U, int NT, typename G>
-hipError_t run_vector(const Weights& w, const TIn* x, int64_t M, int64_t K, int64_t ldx, bool wide, int g,
-                      const W4A16Plan& p, const uint16_t* bias, uint16_t* y, hipStream_t stream) {
-  const auto kernel = vector_kernel<TIn, U, NT, G>;
-  const size_t lds = vector_lds_bytes<U>(int(M));
-  if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
-    if (e != hipSuccess) return e;
-  }
-  // what the chip holds at once: one unit a wave leaves registers for two workgroups a compute unit
-  const int64_t tiles = ceil_div(w.N, 8 * NT), hold = U >= 2 ? 256 : 512;
-  return launch_kernel(kernel, dim3(unsigned(tiles < hold ? tiles : hold)), dim3(kWaves * 64), lds, stream, w, x,
-                       int(M), K, ldx, wide, digits_of(g), int(p.units), int(tiles), bias, y);
-}
-
 template <typename TIn, int U, int NT>
 hipError_t run_vector(const Weights& w, int sg, const TIn* x, int64_t M, int64_t K, int64_t ldx, bool wide,
                       int g, const W4A16Plan& p, const uint16_t* bias, uint16_t* y, hipStream_t stream) {
-  const bool whole = w.row_bytes % 64 == 0;
-  auto run = sg == 128 ? run_vector<TIn, U, NT, Groups<4, true>>
-             : sg == 64 ? (whole ? run_vector<TIn, U, NT, Groups<2, true>> : run_vector<TIn, U, NT, Groups<2, false>>)
-                        : (whole ? run_vector<TIn, U, NT, Groups<1, true>> : run_vector<TIn, U, NT, Groups<1, false>>);
-  return run(w, x, M, K, ldx, wide, g, p, bias, y, stream);
+  const size_t lds = vector_lds_bytes<U>(int(M));
+  // what the chip holds at once: one unit a wave leaves registers for two workgroups a compute unit
+  const int64_t tiles = ceil_div(w.N, 8 * NT), hold = U >= 2 ? 256 : 512;
+  return with_groups(w, sg, [&](auto groups) {
+    const auto kernel = vector_kernel<TIn, U, NT, decltype(groups)>;
+    if (lds > 65536) {
+      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
+      if (e != hipSuccess) return e;
+    }
+    return launch_kernel(kernel, dim3(unsigned(tiles < hold ? tiles : hold)), dim3(kWaves * 64), lds, stream, w, x,
+                         int(M), K, ldx, wide, digits_of(g), int(p.units), int(tiles), bias, y);
+  });
 }
 
 template <typename TIn, int NT>
@@ -600,6 +677,12 @@ hipError_t run_linear(const TIn* x, int64_t M, int64_t K, int64_t ldx, int g, in
                                digits_of(g), p.units, p.rows_padded, op, factor);
   if (e != hipSuccess) return e;
   if (fold) return run_product<1, true, 2>(w, sg, op, factor, p, M, bias, y, stream);
+  // tiles of 32 weight rows once they make a workgroup for each of the 256 compute units
+  if (ceil_div(w.N, 32) * ceil_div(M, 64) < 256) {
+    if (M <= 16) return run_narrow<1>(w, sg, op, factor, p, M, bias, y, stream);
+    if (M <= 32) return run_narrow<2>(w, sg, op, factor, p, M, bias, y, stream);
+    return run_narrow<4>(w, sg, op, factor, p, M, bias, y, stream);
+  }
   if (M <= 16) return run_product<1, false, 2>(w, sg, op, factor, p, M, bias, y, stream);
   if (M <= 32) return run_product<2, false, 2>(w, sg, op, factor, p, M, bias, y, stream);
   return run_product<4, false, 2>(w, sg, op, factor, p, M, bias, y, stream);

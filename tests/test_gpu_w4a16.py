@@ -91,6 +91,19 @@ def test_linear_one_or_two_rows(cr, M, K, N, g, sg, dtype):
     _check(y, x, g, wq, ws, bias)
 
 
+@pytest.mark.parametrize("M,K,N,g,sg,dtype", [
+    # tiles of 32 weight rows (from 256 workgroups on), in the last of them 1 and 31 rows, and tiles of 16
+    (9, 300, 8200, 64, 32, "bf16"), (16, 1200, 8161, 0, 64, "f32"), (32, 520, 8193, 16, 128, "bf16"),
+    (30, 700, 8160, 256, 32, "f32"), (64, 900, 8223, 64, 128, "bf16"), (33, 130, 8170, 0, 32, "f32"),
+    (100, 500, 4200, 16, 64, "bf16"), (130, 260, 2700, 64, 128, "f32"),
+])
+def test_linear_wide_outputs(cr, M, K, N, g, sg, dtype):
+    print(f"\n[case] w4a16 wide M={M} K={K} N={N} g={g} sg={sg} {dtype}", flush=True)
+    x, wq, ws, bias = _inputs(M, K, N, g, sg, torch.float32 if dtype == "f32" else torch.bfloat16, K + N, cr)
+    y = cr.convrot_w4a16_linear(*(t.to(DEV) if isinstance(t, torch.Tensor) else t for t in (x, g, sg, wq, ws, bias)))
+    _check(y, x, g, wq, ws, bias)
+
+
 @pytest.mark.parametrize("M,offset,ld", [(1, 1, 1111), (2, 3, 1003), (7, 1, 1001), (20, 5, 1008), (4, 8, 1016)])
 def test_linear_strided_and_unaligned_rows(cr, M, offset, ld):
     print(f"\n[case] w4a16 rows M={M} offset={offset} ld={ld}", flush=True)
