@@ -36,8 +36,8 @@
  *     acc = exact integer sum over K'.  Output is always bf16.
  *
  * Memory and threading:
- *   - Every pointer argument is a DEVICE pointer owned by the caller, except the host buffer
- *     of convrot_make_rht.  The library never allocates, frees or retains device memory,
+ *   - Every pointer argument is a DEVICE pointer owned by the caller, except the host buffers
+ *     of convrot_make_rht and convrot_rotary_frequencies.  The library never allocates, frees or retains device memory,
  *     except the fixed scratch array of convrot_w4a4_linear_noalloc (below), which the
  *     code object holds on each device it is loaded on.  Its other global state is per-device
  *     caches of the compute-unit count and of that array's address (atomic); every other

@@ -108,8 +108,10 @@ const char* convrot_status_string(int status) {
       return "unsupported: group size must be 16, 64, 256 or 1024, and K' at most 16384 "
              "(g = 16), 32768 (g = 64, 256) or 61440 (g = 1024; 32768 for fp32 input); "
              "with int8 codes 53248 (g = 1024, bf16), 30720 "
-             "(g = 64, 256, fp32) or 28672 (g = 1024, fp32)";
-    case CONVROT_ERR_SHAPE: return "invalid shape (M, N >= 0, K >= 1, ld >= K, no overflow)";
+             "(g = 64, 256, fp32) or 28672 (g = 1024, fp32); the decoding operators' limits stand "
+             "at their declarations in convrot.h";
+    case CONVROT_ERR_SHAPE: return "invalid shape (M, N >= 0, K >= 1, ld >= K, no overflow; sizes and "
+                                    "strides not negative, rows apart)";
     case CONVROT_ERR_NULL: return "a required pointer is NULL";
     case CONVROT_ERR_DTYPE: return "unknown dtype code";
     case CONVROT_ERR_ALIGN: return "pointer or row stride violates the required alignment";
