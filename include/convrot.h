@@ -346,7 +346,7 @@ CONVROT_API int convrot_w4a4_linear_noalloc(const void* x, int32_t x_dtype, int6
  *   0 where s = 0; packing as for int4 above.
  *   y[m][n] = bf16( sum_j s[n][j] sum_{k in group j} code[n][k] xr[m][k] + bias[n] ),
  *   xr = x zero-padded to K' and rotated in windows of g, rounded to fp16 after an exact
- *   power-of-two scaling of every 256 values (relative 2^-12); all sums fp32.
+ *   power-of-two scaling of every 256 values (relative 2^-11); all sums fp32.
  *   A weight group that holds an Inf or a NaN (or overflows in the rotation) gets a NaN scale;
  *   an activation row that holds one gives a NaN output row.
  * --------------------------------------------------------------------------------------- */
@@ -456,7 +456,7 @@ CONVROT_API size_t convrot_kv8_attention_workspace_bytes(int64_t T, int64_t B, i
  * the tokens up to it.  Query head hq reads cached head hq / (Hq / H).
  *   out[t][hq] = bf16( sum_j p_j v_j ), p = softmax_j(scale q.k_j); out contiguous, 16-byte aligned.
  * Scores, statistics and sums are fp32; q (rotated by g as the keys were) and the weights p times the
- * page's value scale enter the products rounded to fp16 (2^-12 relative).  A row that sees no token
+ * page's value scale enter the products rounded to fp16 (2^-11 relative).  A row that sees no token
  * is zero; rows of no sequence are left as they were; a row whose q holds an Inf or a NaN, or that sees a
  * page with a NaN scale, is NaN.  Scales are 0 or at least 2^-80, as append writes them.
  * Results do not depend on the run.  workspace 256-byte aligned, NULL where it needs 0 bytes; T, B, Hq, H,

@@ -406,7 +406,7 @@ __device__ __forceinline__ PageScale scale_of(const Pages& p, int32_t id, uint32
 // R the reference, at most kSlack below max(s_j + log2 vs_j):
 //   w_j = 2^(s_j + log2 vs_j - R + kShift),   o = sum w_j vcode_j,   l = sum w_j / vs_j,
 // so o / l is the answer, the page scale of the values costs nothing in the second product, and w_j
-// rounded to fp16 (2^-12 relative; below 2^-21 of the reference an absolute 2^-32 of it) uses that
+// rounded to fp16 (2^-11 relative; below 2^-21 of the reference an absolute 2^-32 of it) uses that
 // type's range.  The reference moves only when a score passes it by 2^kSlack, so that o is rarely
 // scaled again.
 struct BlockScale {

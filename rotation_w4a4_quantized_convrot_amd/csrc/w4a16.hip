@@ -9,8 +9,8 @@
 // The weights are the traffic: N K'/2 bytes of codes, each read once.  The products run on
 // v_mfma_f32_16x16x32_f16 with the codes exact in fp16 and the activations rounded to fp16
 // after an exact power-of-two scaling per unit of 256 values (decode_device.h, half_range): a
-// rounding of 2^-12 relative to each value, eight times finer than bf16's, where the output is
-// rounded to bf16 (2^-9) anyway; all sums are fp32.
+// rounding of 2^-11 relative to each value, eight times finer than bf16's, where the output is
+// rounded to bf16 (2^-8) anyway; all sums are fp32.
 #include "decode_device.h"
 
 #include <type_traits>
