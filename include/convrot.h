@@ -456,7 +456,10 @@ CONVROT_API size_t convrot_kv8_attention_workspace_bytes(int64_t T, int64_t B, i
  * the tokens up to it.  Query head hq reads cached head hq / (Hq / H).
  *   out[t][hq] = bf16( sum_j p_j v_j ), p = softmax_j(scale q.k_j); out contiguous, 16-byte aligned.
  * Scores, statistics and sums are fp32; q (rotated by g as the keys were) and the weights p times the
- * page's value scale enter the products rounded to fp16 (2^-11 relative).  A row that sees no token
+ * page's value scale enter the products rounded to fp16: 2^-11 relative, and for what is below 2^-21 of the
+ * row's largest weight times scale an absolute 2^-32 of that.  A page of the value scale 0 counts as one of
+ * scale 2^-80 there; its tokens take part in the softmax with values of 0, whatever their codes.  The value
+ * scales that a row sees, 0 apart, lie within 2^100 of one another.  A row that sees no token
  * is zero; rows of no sequence are left as they were; a row whose q holds an Inf or a NaN, or that sees a
  * page with a NaN scale, is NaN.  Scales are 0 or at least 2^-80, as append writes them.
  * Results do not depend on the run.  workspace 256-byte aligned, NULL where it needs 0 bytes; T, B, Hq, H,

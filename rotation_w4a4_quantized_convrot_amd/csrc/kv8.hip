@@ -16,8 +16,9 @@ namespace convrot {
 namespace {
 
 // The least scale that is stored; pages whose values are all below 127 times this hold zeros.
-// Attention divides by scales in fp32: 2^80 times a sum of 2^21 tokens' weights stays finite.
+// Attention divides by scales in fp32: 2^80 times the weights of all tokens, 2^15 each, stays finite.
 constexpr float kLeastScale = 8.271806125530277e-25f;   // 2^-80
+constexpr float kLeastLog = -80.0f;
 
 struct Sequence {
   int64_t row0, n, len;   // first row, new rows, tokens in all (the rows' included)
@@ -409,17 +410,27 @@ __device__ __forceinline__ PageScale scale_of(const Pages& p, int32_t id, uint32
 // rounded to fp16 (2^-11 relative; below 2^-21 of the reference an absolute 2^-32 of it) uses that
 // type's range.  The reference moves only when a score passes it by 2^kSlack, so that o is rarely
 // scaled again.
+// Pages of zeros (vs_j = 0) add to l only.  To the reference they count as pages of the least scale: any
+// larger one would push the weights of pages that have values out of fp16's range, and with none l could
+// overflow.  Their weights are 2^(s_j - R + kShift), at most 2^95 in fp32, and are dropped before the product.
 struct BlockScale {
-  float ks, lv, over_vs;
+  float ks, lv, over_vs;      // lv: for the reference; pages of zeros have 0 in the weights
   // bit 0: the lane's 16 tokens have no page; 1: their values' scale is 0; 2 and 3: so it is for some lane
   int bits;
 };
 
 __device__ __forceinline__ BlockScale settle(const PageScale& page) {
   const bool zero = page.vs == 0.0f;
-  const float lv = zero ? 0.0f : __builtin_amdgcn_logf(page.vs);
-  return BlockScale{page.ks, lv, __builtin_amdgcn_exp2f(-lv),
+  const float lv = zero ? kLeastLog : __builtin_amdgcn_logf(page.vs);
+  return BlockScale{page.ks, lv, zero ? 1.0f : __builtin_amdgcn_exp2f(-lv),
                     (page.there ? 0 : 1) | (zero ? 2 : 0) | (__any(!page.there) ? 4 : 0) | (__any(zero) ? 8 : 0)};
+}
+
+// A sum l under a reference that is higher by -d >= 0: l 2^d in two steps, since l may be as large as 2^d is
+// small (a share that saw pages of zeros only, next to one of large values) and 2^d alone would be 0.
+__device__ __forceinline__ float lowered(float l, float d) {
+  const float half = __builtin_amdgcn_exp2f(0.5f * d);
+  return l * half * half;
 }
 
 // First half: scores of tokens that are not there or not seen to -infinity (`ragged`: there are some;
@@ -460,8 +471,8 @@ __device__ __forceinline__ void refer(float4_t (&s)[4][RT], const BlockScale& bs
     for (int rt = 0; rt < RT; ++rt) {
       const float now = fmaxf(m[rt], high[rt]);
       const float down = __builtin_amdgcn_exp2f(m[rt] - now);
+      l[rt] = lowered(l[rt], m[rt] - now);
       m[rt] = now;
-      l[rt] *= down;
 #pragma unroll
       for (int dt = 0; dt < TILES; ++dt) o[dt][rt] *= down;
     }
@@ -475,7 +486,7 @@ __device__ __forceinline__ void weigh(const float4_t (&s)[4][RT], const BlockSca
   float4_t w[4][RT];
   float add[RT];
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) add[rt] = bs.lv - m[rt] + kShift;
+  for (int rt = 0; rt < RT; ++rt) add[rt] = (bs.bits & 2 ? 0.0f : bs.lv) - m[rt] + kShift;
 #pragma unroll
   for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -713,7 +724,7 @@ __global__ __launch_bounds__(256, DT <= 128 ? 2 : 1) void few_rows_kernel(Attent
       float sum = 0.0f;
 #pragma unroll
       for (int p = 0; p < kPhases; ++p)
-        sum += wave_l[t + p * TILES][i] * __builtin_amdgcn_exp2f(wave_m[t + p * TILES][i] - top);
+        sum += lowered(wave_l[t + p * TILES][i], wave_m[t + p * TILES][i] - top);
       const int64_t row = (w.seq.row0 + r / G) * a.Hq + w.h * G + r % G;
       if (a.partial != nullptr && n == 0) a.stats[w.split * a.rows + row] = make_float2(top, sum);
       const float over_l = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -1001,7 +1012,7 @@ __global__ __launch_bounds__(256) void join_splits_kernel(Kv8Batch batch, int Hq
   float sum = 0.0f;
   for (int s = lane; s < splits; s += 64) {
     const float2 st = stats[s * rows + row];
-    sum += st.y * __builtin_amdgcn_exp2f(st.x - top);
+    sum += lowered(st.y, st.x - top);
   }
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);

@@ -498,3 +498,49 @@ def test_block_run_together_graph_and_streams(cr):
         torch.cuda.synchronize()
         assert torch.equal(y, eager[step]), step
         run()[0][-1].sum().item()                            # eager work of the program in between
+
+
+def zero_page_case(rows, D, G, page, vs, nats, at, seed=0):
+    """One sequence of five pages and a bit, new rows at its end; the values of page `at` have the scale 0 (its codes
+    are of earlier use), those of the others the scale vs; the first head's scores in page `at` are `nats` above 0,
+    where the others' lie about."""
+    gen = torch.Generator().manual_seed(seed + rows + D)
+    length = 5 * page + 3 + rows
+    table, pages = paging([length], page, gen)
+    cache = cache_of(pages, 1, page, D, gen)
+    kc, ks, _, vscale = cache
+    kc[..., 0] = 0
+    ks.fill_(2.0 ** -10)
+    vscale.fill_(vs)
+    q = torch.randn((rows, G, D), generator=gen).to(torch.bfloat16)
+    hot = int(table[0, at])
+    kc[hot] = 0
+    kc[hot, ..., 0] = 127
+    ks[hot] = 2.0 ** -4
+    vscale[hot] = 0
+    q[..., 0] = nats * math.sqrt(D) / (127 * 2.0 ** -4)
+    return q, cum([rows]), torch.tensor([length], dtype=torch.int32), table, cache
+
+
+@pytest.mark.parametrize("rows,D,G,page", [(1, 64, 4, 16), (5, 128, 4, 16), (8, 96, 8, 32), (1, 256, 8, 64),
+                                           (60, 64, 2, 16), (40, 128, 4, 32), (70, 256, 1, 16)])
+@pytest.mark.parametrize("max_len", [1, 4000])               # one split of the tokens, and several
+def test_attention_zero_value_pages_next_to_others(cr, rows, D, G, page, max_len):
+    """Pages of zeros count in the softmax and give nothing; the others keep their accuracy beside them, whatever
+    the scales: rounded weights are relative to the largest weight times value scale, and pages of zeros have none."""
+    print(f"\n[case] attention zero pages rows={rows} D={D} G={G} page={page} max_len={max_len}", flush=True)
+    for vs in (2.0 ** -7, 2.0 ** -20, 2.0 ** -40, 2.0 ** -79, 2.0 ** 60):
+        # a page of zeros counts as one of the least scale, 2^-80; a weight keeps its 11 bits down to 2^-21 of the largest
+        for nats in (0, 5, 10, 15, 18) if vs >= 2.0 ** -40 else (0, 5, 10):
+            for at in (0, 3):                                # the first page that a row sees, and a later one
+                q, cu, ln, table, cache = zero_page_case(rows, D, G, page, vs, nats, at)
+                out = cr.convrot_kv8_attention(q.to(DEV), cu.to(DEV), ln.to(DEV), table.to(DEV), *to(cache), max_len=max_len)
+                ref, size, mean = O.attention(q, cu, ln, table, *cache, 0, 1 / math.sqrt(D))
+                # the tolerance of check_attention, in units of the value scale instead of its 1e-30
+                d = (2.0 ** -11 + (D + 16) * 2.0 ** -24 + 2.0 ** -20) * size + 2.0 ** -18
+                e = torch.expm1(2 * d) + 2.0 ** -11 + 2.0 ** -16
+                off, tol = (out.cpu().double() - ref).abs(), 2.0 ** -8 * ref.abs() + 2 * e[..., None] * mean
+                assert bool((off <= tol).all()), f"vs={vs} nats={nats} at={at}: {(off / tol).max().item():.2f} of the tolerance"
+    q, cu, ln, table, cache = zero_page_case(rows, D, G, page, 0.0, 3, 2)      # nothing but zeros
+    out = cr.convrot_kv8_attention(q.to(DEV), cu.to(DEV), ln.to(DEV), table.to(DEV), *to(cache), max_len=max_len)
+    assert int(out.abs().max().item()) == 0
