@@ -931,29 +931,37 @@ __global__ __launch_bounds__(512) void many_rows_kernel(AttentionArgs a, Kv8Batc
           lds_barrier();
           __builtin_amdgcn_s_setprio(1);
           // both products as one run of matrix instructions, each operand block read kAhead blocks before
-          // its use, and the other work in pieces between them; the compiler keeps this order
+          // its use, and the other work in pieces between them; the compiler keeps this order.  A loop for
+          // each product: as one of 64 rounds (heads above 128) the compiler does not write it out, and
+          // every array that it indexes moves to scratch memory (3x900 rows over 6000 tokens, 16 / 4
+          // heads of 256: 69 ms so, 261 us in two loops)
           const uint8_t* const values = value_lds + (i & 1) * kHalf;
           const uint8_t* const keys = key_lds + ((i + 1) & 1) * kHalf;
           half8 ring[kAhead];
 #pragma unroll
           for (int j = 0; j < kAhead; ++j) ring[j] = value_block(values, j);
-#pragma unroll
-          for (int j = 0; j < 2 * kReads; ++j) {
-            const half8 operand = ring[j % kAhead];
-            if (j < kReads) {
-#pragma unroll
-              for (int rt = 0; rt < RT; ++rt)
-                o[j % kTilesD][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand, j < kTilesD ? w0[rt] : w1[rt],
-                                                                           o[j % kTilesD][rt], 0, 0, 0);
-            } else {
-              score_step(operand, j - kReads);
-            }
-            if (j + kAhead < kReads) ring[j % kAhead] = value_block(values, j + kAhead);
-            else if (j + kAhead < 2 * kReads) ring[j % kAhead] = key_block(keys, j + kAhead - kReads);
+          const auto beside = [&](int j) {
 #pragma unroll
             for (int p = 0; p < kPieceCount; ++p)
               if (p * 2 * kReads / kPieceCount == j) piece(i, p);
             __builtin_amdgcn_sched_barrier(0);
+          };
+#pragma unroll
+          for (int j = 0; j < kReads; ++j) {
+            const half8 operand = ring[j % kAhead];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+              o[j % kTilesD][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand, j < kTilesD ? w0[rt] : w1[rt],
+                                                                         o[j % kTilesD][rt], 0, 0, 0);
+            ring[j % kAhead] = j + kAhead < kReads ? value_block(values, j + kAhead) : key_block(keys, j + kAhead - kReads);
+            beside(j);
+          }
+#pragma unroll
+          for (int j = kReads; j < 2 * kReads; ++j) {
+            const half8 operand = ring[j % kAhead];
+            score_step(operand, j - kReads);
+            if (j + kAhead < 2 * kReads) ring[j % kAhead] = key_block(keys, j + kAhead - kReads);
+            beside(j);
           }
           __builtin_amdgcn_s_setprio(0);
           lds_barrier();
