@@ -358,7 +358,8 @@ __device__ __forceinline__ Pages pages_of(const Kv8Batch& batch, const Kv8Cache&
 // Sixteen values of query row r of a (sequence, cached head), rotated and scaled into fp16's range, to
 // 16 places of LDS; `factor` takes the row's score scale, in powers of two.  A row of 16 lanes
 // holds the row.  A negative scale's sign goes to the query, so that score scales are never
-// negative.
+// negative.  A row that holds an Inf or a NaN becomes NaN as a whole: unrotated, an Inf that meets codes of
+// one sign would make scores of -Inf, which is how tokens that are not seen are marked.
 template <typename TIn, int DT>
 __device__ __forceinline__ void stage_query(const AttentionArgs& a, const Kv8Cache& cache, const Work& w, int64_t r,
                                             int n, _Float16* row, float* factor) {
@@ -369,8 +370,9 @@ __device__ __forceinline__ void stage_query(const AttentionArgs& a, const Kv8Cac
   float v[16];
   load16<TIn>(p, there ? 16 : 0, a.q_wide, v);
   float up, back;
-  half_range(row_max(abs_max16(v)), a.digits, &up, &back);
-  up = a.scale < 0.0f ? -up : up;
+  const uint32_t bits = row_max(abs_max16(v));
+  half_range(bits, a.digits, &up, &back);
+  up = bits >= 0x7F800000u ? back : a.scale < 0.0f ? -up : up;        // back is NaN there
 #pragma unroll
   for (int e = 0; e < 16; ++e) v[e] *= up;
   rotate16(v, a.digits);

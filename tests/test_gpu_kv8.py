@@ -544,3 +544,29 @@ def test_attention_zero_value_pages_next_to_others(cr, rows, D, G, page, max_len
     q, cu, ln, table, cache = zero_page_case(rows, D, G, page, 0.0, 3, 2)      # nothing but zeros
     out = cr.convrot_kv8_attention(q.to(DEV), cu.to(DEV), ln.to(DEV), table.to(DEV), *to(cache), max_len=max_len)
     assert int(out.abs().max().item()) == 0
+
+
+@pytest.mark.parametrize("new,G,D", [([1, 1, 1], 2, 64), ([5, 1, 9], 4, 128), ([80, 70, 33], 2, 64), ([90, 40, 17], 1, 256)])
+def test_attention_infinite_queries_without_rotation(cr, new, G, D):
+    """An Inf in a query meets codes of one sign: its scores are all -Inf, and its row NaN all the same."""
+    print(f"\n[case] attention infinite queries new={new} G={G} D={D}", flush=True)
+    gen = torch.Generator().manual_seed(D)
+    lens = [1 + n for n in new]
+    table, pages = paging(lens, 16, gen)
+    cache = cache_of(pages, 1, 16, D, gen)
+    cache[0][..., 5] = -3
+    q = torch.randn((sum(new), G, D), generator=gen)
+    args = [t.to(DEV) for t in (cum(new), torch.tensor(lens, dtype=torch.int32), table, *cache)]
+    good = cr.convrot_kv8_attention(q.to(DEV), *args, max_new=max(new)).cpu()
+    for value, scale in ((float("inf"), 0.1), (-float("inf"), -0.1)):
+        rows = [0, new[0], sum(new) - 1]
+        bad = q.clone()
+        bad[rows, 0, 5] = value
+        out = cr.convrot_kv8_attention(bad.to(DEV), *args, scale=scale, max_new=max(new)).cpu()
+        assert bool(out[rows, 0].isnan().all()), value
+        if G > 1:
+            assert bool(out[:, 1:].isfinite().all())
+        out = cr.convrot_kv8_attention(bad.to(DEV), *args, max_new=max(new)).cpu()
+        assert bool(out[rows, 0].isnan().all()), value
+        good[rows, 0] = out[rows, 0]
+        assert torch.equal(out.nan_to_num(), good.nan_to_num())
