@@ -394,9 +394,10 @@ struct PageScale {
   bool there;
 };
 
-// A token's place from the share's first one; what is far beyond it all the same.
+// A token's place from the share's first one, -1 for all before it.  Lengths are int32, so the places of a
+// share's tokens are too, to the end of its last block of 64; what is compared with them stays at 2^31 - 1.
 __device__ __forceinline__ int from_here(int64_t token, int64_t first) {
-  return int(max(min(token - first, int64_t(1) << 30), int64_t(-1)));
+  return int(max(min(token - first, int64_t(0x7FFFFFFF)), int64_t(-1)));
 }
 
 __device__ __forceinline__ PageScale scale_of(const Pages& p, int32_t id, uint32_t base, uint32_t off) {
@@ -670,7 +671,7 @@ __global__ __launch_bounds__(256, DT <= 128 ? 2 : 1) void few_rows_kernel(Attent
       __builtin_amdgcn_sched_barrier(0);
       const BlockScale bs = settle(page);
       const int some = __builtin_amdgcn_readfirstlane(bs.bits);
-      const bool ragged = base + 63 > all_see || base + 64 > rel_limit || (some & 4);
+      const bool ragged = base + 63 > all_see || base + 63 >= rel_limit || (some & 4);
       half8 w0[RT], w1[RT];
       float mul[RT];
       refer(s, bs, ragged, base + 16 * c, rel_limit, row_scale, sees, m, l, o, mul);
@@ -923,7 +924,7 @@ __global__ __launch_bounds__(512) void many_rows_kernel(AttentionArgs a, Kv8Batc
       if (active) {
         for (int i = 0; i < count; ++i) {
           const int some = __builtin_amdgcn_readfirstlane(bs.bits);
-          const bool ragged = i * 64 + 63 > all_see || i * 64 + 64 > rel_limit || (some & 4);
+          const bool ragged = i * 64 + 63 > all_see || i * 64 + 63 >= rel_limit || (some & 4);
           float mul[RT];
           half8 w0[RT], w1[RT];
           refer(s, bs, ragged, i * 64 + 16 * c, rel_limit, row_scale, sees, m, l, o, mul);

@@ -570,3 +570,29 @@ def test_attention_infinite_queries_without_rotation(cr, new, G, D):
         assert bool(out[rows, 0].isnan().all()), value
         good[rows, 0] = out[rows, 0]
         assert torch.equal(out.nan_to_num(), good.nan_to_num())
+
+
+def test_attention_share_of_more_than_2_to_the_30_tokens(cr):
+    """A sequence of 2^30 + 200 tokens whose pages are all one page but the last two, in one share (the hint says
+    so).  The last tokens score far above all others: their values are the answer."""
+    print("\n[case] attention 2^30 tokens in a share", flush=True)
+    H, D, page = 1, 16, 128
+    L = (1 << 30) + 200
+    kc = torch.zeros((4, H, page, D), dtype=torch.int8)
+    vc = torch.ones((4, H, D, page), dtype=torch.int8)
+    kc[1:3, ..., 0] = 127
+    vc[1], vc[2], vc[3] = 50, 90, 17
+    ks, vs = torch.ones((4, H)), torch.ones((4, H))
+    table = torch.zeros((1, (1 << 23) + 2), dtype=torch.int32, device=DEV)
+    table[0, -2:] = torch.tensor([1, 2], dtype=torch.int32)
+    q = torch.zeros((2, 1, D), device=DEV)
+    q[:, 0, 0] = 1.0
+    # row 0 sees page 1 and 71 tokens of page 2, row 1 one more
+    lens, cu = torch.tensor([L], dtype=torch.int32, device=DEV), cum([2]).to(DEV)
+    assert cr.convrot_kv8_attention_workspace_bytes(2, 1, 1, H, D, 2, 1) == 0
+    out = cr.convrot_kv8_attention(q, cu, lens, table, *to([kc, ks, vc, vs]), scale=1.0, max_new=2, max_len=1)
+    torch.cuda.synchronize()
+    # off by the weights' rounding to fp16 and their exp2 at most, 2^-11 + 2^-16, and the output's to bf16
+    for row, second in ((0, 71), (1, 72)):
+        want = (128 * 50 + second * 90) / (128 + second)     # e^127 to 1 against 2^30 others
+        assert bool(((out[row].cpu().double() - want).abs() <= (2.0 ** -8 + 2 * (2.0 ** -11 + 2.0 ** -16)) * want).all())
