@@ -596,3 +596,53 @@ def test_attention_share_of_more_than_2_to_the_30_tokens(cr):
     for row, second in ((0, 71), (1, 72)):
         want = (128 * 50 + second * 90) / (128 + second)     # e^127 to 1 against 2^30 others
         assert bool(((out[row].cpu().double() - want).abs() <= (2.0 ** -8 + 2 * (2.0 ** -11 + 2.0 ** -16)) * want).all())
+
+
+SPLIT_ATTENTION = [
+    # lens, new, Hq, H, D, page: 17 to 32 and 33 to 64 rows of a cached head, in one split and in several of some
+    # blocks each, and more rows over long contexts, whose later shares start inside the sequence
+    ([700, 333], [3, 4], 16, 2, 64, 32), ([3000, 1300], [4, 3], 8, 1, 128, 16), ([1500, 90], [3, 3], 8, 1, 256, 64),
+    ([700, 333], [7, 5], 8, 1, 64, 16), ([2600, 1100], [8, 6], 16, 2, 128, 128), ([1900], [7], 8, 1, 256, 32),
+    ([5000], [100], 2, 1, 64, 64), ([4100, 900], [100, 37], 2, 1, 128, 32), ([3000], [100], 2, 1, 256, 16),
+    ([3500], [70], 4, 2, 96, 128),
+]
+
+
+@pytest.mark.parametrize("lens,new,Hq,H,D,page", SPLIT_ATTENTION)
+@pytest.mark.parametrize("split", [False, True])
+def test_attention_shares_of_several_blocks(cr, lens, new, Hq, H, D, page, split):
+    print(f"\n[case] attention shares lens={lens} new={new} H={Hq}/{H} D={D} page={page} split={split}", flush=True)
+    gen = torch.Generator().manual_seed(sum(lens) + D)
+    table, pages = paging(lens, page, gen)
+    cache = cache_of(pages, H, page, D, gen)
+    q = torch.randn((sum(new), Hq, D), generator=gen).to(torch.bfloat16)
+    cu, ln = cum(new), torch.tensor(lens, dtype=torch.int32)
+    max_len = max(lens) if split else 1
+    need = cr.convrot_kv8_attention_workspace_bytes(sum(new), len(new), Hq, H, D, max(new), max_len)
+    assert (need > 0) == (split and max_len >= 1024)         # no share has fewer than 8 blocks of 64 tokens
+    out = cr.convrot_kv8_attention(q.to(DEV), cu.to(DEV), ln.to(DEV), table.to(DEV), *to(cache), max_new=max(new),
+                                   max_len=max_len)
+    check_attention(out, q, cu, ln, table, cache, 0, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("lens,new,Hq,H,D", [([300], [1], 8, 1, 256), ([1500], [90], 2, 1, 128), ([200], [90], 1, 1, 256)])
+def test_attention_of_large_workgroups_in_a_graph(cr, lens, new, Hq, H, D):
+    """Kernels that ask for more than 64 KB of LDS, first called inside a capture; lengths change on the device."""
+    print(f"\n[case] attention graph lens={lens} new={new} D={D}", flush=True)
+    gen = torch.Generator().manual_seed(D + sum(lens))
+    table, pages = paging(lens, 32, gen)
+    cache = cache_of(pages, H, 32, D, gen)
+    q = torch.randn((sum(new), Hq, D), generator=gen).to(torch.bfloat16)
+    dq, dcu, dln, dt = q.to(DEV), cum(new).to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV), table.to(DEV)
+    dc = to(cache)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = cr.convrot_kv8_attention(dq, dcu, dln, dt, *dc, max_new=max(new), max_len=max(lens))
+    for step in range(3):
+        dln.copy_(torch.tensor([n - 7 * step for n in lens], dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = cr.convrot_kv8_attention(dq, dcu, dln, dt, *dc, max_new=max(new), max_len=max(lens))
+        assert torch.equal(out, want), step
+        check_attention(out, q, cum(new), dln.cpu(), table, cache, 0, 1 / math.sqrt(D))
