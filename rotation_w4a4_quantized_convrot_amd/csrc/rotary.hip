@@ -36,12 +36,14 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int head
   const int64_t t = blockIdx.x;
   const double pos = double(a.pos[t]);
   for (int i = threadIdx.x; i < a.R / 2; i += kThreads) {
-    // pos * inv_freq / 2 pi in two fp64 pieces: exact to about 2^-50 of a turn for positions
-    // below 2^29 (53 - 24 bits), where the product below is exact
+    // pos * inv_freq / 2 pi with the product and the turns in two fp64 pieces each: good to about 2^-50 of
+    // a turn for positions below 2^53, which fp64 holds (from 2^29 on, 53 - 24 bits, the product has a
+    // second piece)
     constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591104e-18;   // 1 / (2 pi)
-    const double p = pos * double(a.inv_freq[i]);
+    const double f = double(a.inv_freq[i]);
+    const double p = pos * f, p_lo = __builtin_fma(pos, f, -p);
     const double hi = p * kHi;
-    const double lo = __builtin_fma(p, kHi, -hi) + p * kLo;
+    const double lo = __builtin_fma(p, kHi, -hi) + __builtin_fma(p, kLo, p_lo * kHi);
     const double frac = (hi - __builtin_rint(hi)) + lo;
     float s, c;
     sincospif(float(2.0 * frac), &s, &c);

@@ -131,3 +131,36 @@ def test_rotary_empty_and_graph(cr):
         torch.cuda.synchronize()
         want, _ = cr.convrot_rotary(q, None, pos, inv)
         assert torch.equal(out, want), step
+
+
+def _exact_turns(pos, inv):
+    """cos and sin of pos * inv, the product exact and its turns taken off in 60 digits."""
+    from decimal import Decimal, localcontext
+    with localcontext() as ctx:
+        ctx.prec = 60
+        turn = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+        rest = lambda p, f: float(Decimal(p) * Decimal(f) % turn)  # noqa: E731
+        angle = torch.tensor([[rest(p, f) for f in inv.double().tolist()] for p in pos.tolist()], dtype=torch.float64)
+    return angle.cos(), angle.sin()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("top", [2 ** 31, 2 ** 40, 2 ** 53 - 1])
+def test_rotary_far_positions_keep_their_accuracy(cr, top, interleaved):
+    """Positions up to the largest that fp64 holds: the same tolerance as near ones."""
+    print(f"\n[case] rotary positions up to {top} interleaved={interleaved}", flush=True)
+    gen = torch.Generator().manual_seed(7)
+    T, H, R = 40, 2, 64
+    x = torch.randn((T, H, R), generator=gen)
+    pos = torch.randint(top // 2, top + 1, (T,), generator=gen)
+    pos[0], pos[1] = top, -top
+    inv = cr.convrot_rotary_frequencies(R)
+    y, _ = cr.convrot_rotary(x.to(DEV), None, pos.to(DEV), inv.to(DEV), interleaved)
+    cos, sin = (t[:, None] for t in _exact_turns(pos, inv))
+    a, b = (x[..., 0::2], x[..., 1::2]) if interleaved else (x[..., :R // 2], x[..., R // 2:])
+    a, b = a.double(), b.double()
+    u, v = a * cos - b * sin, b * cos + a * sin
+    ref = torch.stack((u, v), dim=-1).flatten(-2) if interleaved else torch.cat((u, v), dim=-1)
+    off = (y.cpu().double() - ref).abs()
+    tol = _bound(x, ref, R, interleaved, 1.0)
+    assert bool((off <= tol).all()), f"worst {(off / tol).max().item():.3g} of the tolerance"
