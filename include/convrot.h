@@ -397,8 +397,10 @@ CONVROT_API int convrot_rotary_frequencies(int64_t R, double base, int32_t scali
  * the others are copied.  inverse != 0 turns by -angle: the transpose, so the gradient of the
  * outputs becomes that of the inputs (factor is applied as well), and keys can be moved.
  * Strides are in elements, of tokens (_t) and heads (_h); elements of a head are contiguous.
- * Outputs may be the inputs themselves (the same pointer and strides), but not overlap them
- * otherwise.  Hk = 0 or Hq = 0: no such tensor (its pointers may be NULL).  dtype of all four.
+ * An output may be its own input (the same pointer and strides); otherwise its rows must not meet one
+ * another, nor those of any tensor of the call (SHAPE).  Views of one buffer that lie between one
+ * another are told apart where they have the same token stride; where they have not, they count as
+ * meeting.  Hk = 0 or Hq = 0: no such tensor (its pointers may be NULL).  dtype of all four.
  * inv_freq fp32 [R/2], pos int64 [T].  T = 0 is a no-op.  R even, 2 <= R <= D <= 1024; at most 65535
  * heads and 16777215 tokens.  Errors: DTYPE, SHAPE, UNSUPPORTED, NULL, ALIGN, HIP. */
 CONVROT_API int convrot_rotary(const void* q, int64_t q_t, int64_t q_h, void* q_out, int64_t qo_t, int64_t qo_h,

@@ -74,6 +74,54 @@ bool attention_plannable(int64_t T, int64_t B, int64_t Hq, int64_t H) {
   return T <= kIntMax / Hq && B <= kMaxThreads / 256 / (2 * H);
 }
 
+// Rows of D elements, one for each of T tokens and `heads` heads, as they stand in memory.
+struct Rows {
+  uintptr_t at;
+  int64_t t, h, heads;
+};
+
+// Elements from the first row's first to behind the last row's last; -1 past what memory can hold.
+int64_t span_of(const Rows& r, int64_t T, int64_t D) {
+  const __int128 n = __int128(T - 1) * r.t + __int128(r.heads - 1) * r.h + D;
+  return n < (int64_t(1) << 58) ? int64_t(n) : -1;
+}
+
+// Whether two rows (t, h) of a tensor meet, with head and token strides of at least D: some k heads' step is
+// within D of some number of tokens' steps.
+bool rows_meet(const Rows& r, int64_t T, int64_t D) {
+  if (T == 1 || r.heads == 1 || r.t - (r.heads - 1) * r.h >= D || r.h - (T - 1) * r.t >= D) return false;
+  for (int64_t k = 1; k < r.heads; ++k) {
+    const int64_t below = k * r.h / r.t, off = k * r.h - below * r.t;
+    if ((below >= 1 && below < T && off < D) || (below + 1 < T && r.t - off < D)) return true;
+  }
+  return false;
+}
+
+// Whether a row of a meets a row of b, elements of `size` bytes.  Exact where the tensors have one token stride
+// (views of one buffer do) and up to 2^20 pairs of heads; else spans that reach into one another count.
+bool rows_meet(const Rows& a, const Rows& b, int64_t T, int64_t D, int64_t size) {
+  const int64_t an = span_of(a, T, D), bn = span_of(b, T, D);
+  if (a.at + uintptr_t(an * size) <= b.at || b.at + uintptr_t(bn * size) <= a.at) return false;
+  if (T > 1 && a.t != b.t) return true;
+  const int64_t step = T > 1 ? a.t : 0, from = (int64_t(b.at) - int64_t(a.at)) / size;
+  // the heads of a token side by side in each, and b's in the gap between a's
+  const int64_t aw = (a.heads - 1) * a.h + D, bw = (b.heads - 1) * b.h + D;
+  if (step > 0) {
+    const int64_t gap = (from % step + step) % step;
+    if (gap >= aw && gap + bw <= step) return false;
+  }
+  if (a.heads * b.heads > 1 << 20) return true;
+  for (int64_t i = 0; i < a.heads; ++i)
+    for (int64_t j = 0; j < b.heads; ++j) {
+      const int64_t off = from + j * b.h - i * a.h;           // tokens apart by k: off + k step
+      if (off > -D && off < D) return true;
+      if (step == 0) continue;
+      const int64_t far = off < 0 ? -off : off, below = far / step, rest = far - below * step;
+      if ((below < T && rest < D) || (below + 1 < T && step - rest < D)) return true;
+    }
+  return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -175,18 +223,35 @@ int convrot_rotary(const void* q, int64_t q_t, int64_t q_h, void* q_out, int64_t
     if (!stride_ok(p.in_t) || !stride_ok(p.in_h) || !stride_ok(p.out_t) || !stride_ok(p.out_h))
       return CONVROT_ERR_SHAPE;
     // rows of the output must not meet
-    if ((p.heads > 1 && p.out_h < D) || (T > 1 && p.out_t < D)) return CONVROT_ERR_SHAPE;
+    const Rows out{reinterpret_cast<uintptr_t>(p.out), p.out_t, p.out_h, p.heads};
+    if ((p.heads > 1 && p.out_h < D) || (T > 1 && p.out_t < D) || span_of(out, T, D) < 0 || rows_meet(out, T, D))
+      return CONVROT_ERR_SHAPE;
     if (p.in == p.out && ((T > 1 && p.in_t != p.out_t) || (p.heads > 1 && p.in_h != p.out_h)))
       return CONVROT_ERR_SHAPE;
+    if (span_of(Rows{0, p.in_t, p.in_h, p.heads}, T, D) < 0) return CONVROT_ERR_SHAPE;
   }
   if (T == 0 || Hq + Hk == 0) return CONVROT_OK;
-  if (pos == nullptr || inv_freq == nullptr) return CONVROT_ERR_NULL;
-  if (!aligned(pos, 8) || !aligned(inv_freq, 4)) return CONVROT_ERR_ALIGN;
   for (const auto& p : part) {
     if (p.heads == 0) continue;
     if (p.in == nullptr || p.out == nullptr) return CONVROT_ERR_NULL;
     if (!aligned(p.in, size) || !aligned(p.out, size)) return CONVROT_ERR_ALIGN;
   }
+  // an output is its own input, or meets no tensor of the call
+  for (int i = 0; i < 2; ++i) {
+    const auto &p = part[i], &other = part[1 - i];
+    if (p.heads == 0) continue;
+    const Rows out{reinterpret_cast<uintptr_t>(p.out), p.out_t, p.out_h, p.heads};
+    const Rows in{reinterpret_cast<uintptr_t>(p.in), p.in_t, p.in_h, p.heads};
+    if (p.in != p.out && rows_meet(out, in, T, D, int64_t(size))) return CONVROT_ERR_SHAPE;
+    if (other.heads == 0) continue;
+    if (rows_meet(out, Rows{reinterpret_cast<uintptr_t>(other.in), other.in_t, other.in_h, other.heads}, T, D,
+                  int64_t(size)) ||
+        rows_meet(out, Rows{reinterpret_cast<uintptr_t>(other.out), other.out_t, other.out_h, other.heads}, T, D,
+                  int64_t(size)))
+      return CONVROT_ERR_SHAPE;
+  }
+  if (pos == nullptr || inv_freq == nullptr) return CONVROT_ERR_NULL;
+  if (!aligned(pos, 8) || !aligned(inv_freq, 4)) return CONVROT_ERR_ALIGN;
   convrot::RotaryArgs a{{q, q_out, q_t, q_h, qo_t, qo_h, int(Hq)}, {k, k_out, k_t, k_h, ko_t, ko_h, int(Hk)},
                         pos, inv_freq, factor, int(D), int(R), interleaved != 0, inverse != 0};
   return status_of(convrot::launch_rotary(a, dtype, T, static_cast<hipStream_t>(stream)));

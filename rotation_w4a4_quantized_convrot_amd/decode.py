@@ -162,6 +162,25 @@ def _span(t: torch.Tensor) -> Tuple[int, int]:
     return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
 
 
+def _meet(x: torch.Tensor, y: torch.Tensor) -> bool:
+    """Whether elements of two [tokens, heads, D] tensors are the same memory; spans that reach into one
+    another count where the token strides differ."""
+    (a, b), (c, d) = _span(x), _span(y)
+    if b <= c or d <= a:
+        return False
+    T, _, D = x.shape
+    step = x.stride(0) if T > 1 else 0
+    if T > 1 and y.stride(0) != step:
+        return True
+    (hx, sx), (hy, sy), off = (x.shape[1], x.stride(1)), (y.shape[1], y.stride(1)), (c - a) // x.element_size()
+    if step and off % step >= (hx - 1) * sx + D and off % step + (hy - 1) * sy + D <= step:
+        return False                                       # the heads of a token side by side in each
+    apart = {j * sy - i * sx for i in range(hx) for j in range(hy)}
+    near = lambda n: any(abs(n + k * step) < D for k in ((-n // step, -n // step + 1) if step else (0,))  # noqa: E731
+                         if abs(k) < T)
+    return any(near(off + n) for n in apart)
+
+
 def _rotary_out(x: torch.Tensor, out: Optional[torch.Tensor], name: str) -> None:
     if out is None:
         return
@@ -169,10 +188,9 @@ def _rotary_out(x: torch.Tensor, out: Optional[torch.Tensor], name: str) -> None
     if out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError(f"{name} must have shape {tuple(x.shape)} and dtype {x.dtype}, got "
                          f"{tuple(out.shape)} and {out.dtype}")
-    if out.data_ptr() == x.data_ptr() and out.stride() == x.stride():
+    if out.data_ptr() == x.data_ptr() and all(n == 1 or s == t for n, s, t in zip(x.shape, x.stride(), out.stride())):
         return
-    (a, b), (c, d) = _span(x), _span(out)
-    if x.numel() and x.device == out.device and a < d and c < b:
+    if x.numel() and x.device == out.device and _meet(x, out):
         raise ValueError(f"{name} overlaps its input without being it")
 
 
@@ -180,8 +198,9 @@ def convrot_rotary(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor
                    interleaved: bool = False, factor: float = 1.0, inverse: bool = False,
                    q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
     """q [T, Hq, D] and k [T, Hk, D] (or None), bf16/fp32, turned by pos int64 [T] times inv_freq fp32
-    [R/2] -> (q_out, k_out), new tensors unless given; the inputs themselves may be given.  inverse
-    turns back, which is the gradient's direction too."""
+    [R/2] -> (q_out, k_out), new tensors unless given; the inputs themselves may be given, and views beside
+    them, but no output may overlap another tensor of the call.  inverse turns back, which is the
+    gradient's direction too."""
     T, Hq, D = _heads(q, "q")
     if k is not None:
         if _heads(k, "k")[0] != T or k.shape[2] != D or k.dtype != q.dtype:

@@ -260,3 +260,56 @@ def test_sizes_past_a_launch_are_refused(lib):
     nbytes = cr.convrot_kv8_attention_workspace_bytes
     assert nbytes(2 ** 27, 2 ** 30, 2 ** 15, 2 ** 15, 128, 2 ** 27, 1000) == 0      # 2^64 workgroups
     assert nbytes(2 ** 31 - 1, 2 ** 22, 2 ** 15, 1, 256, 2 ** 31 - 1, 2 ** 31 - 1) == 0
+
+
+def test_rotary_outputs_that_meet_are_refused(lib):
+    """Rows of an output that meet one another, or another tensor of the call, would be written by several
+    workgroups at once; views that lie between one another without meeting are taken (those calls end at their
+    missing positions, which are looked at last)."""
+    D, T = 16, 3
+    S = 2                                                     # bytes of a bf16 element
+
+    def call(q, qo, k=None, ko=None, T=T, pos=A):
+        """q, qo, k, ko: (offset in elements, token stride, head stride, heads)"""
+        part = lambda i, o: (A + S * i[0], i[1], i[2], A + S * o[0], o[1], o[2], i[3])  # noqa: E731
+        none = (None, 0, 0, None, 0, 0, 0)
+        return lib.convrot_rotary(*part(q, qo), *(part(k, ko) if k else none), 1, T, D, D, pos, A, 0,
+                                  ctypes.c_float(1.0), 0, None)
+
+    far = 1 << 20
+    refused = lambda *a, **kw: call(*a, **kw) == E.CONVROT_ERR_SHAPE  # noqa: E731
+    # rows of the output among themselves
+    assert refused((0, 64, D, 4), (far, D, D, 4)) and refused((0, 64, D, 4), (far, 3 * D, 2 * D - 1, 3))
+    assert refused((0, 64, D, 4), (far, 40, 80, 4))           # two tokens on are one head on
+    assert refused((0, 64, D, 2), (far, 1 << 46, 1 << 46, 2), T=1 << 23)       # past what memory holds
+    # q_out against q
+    assert refused((0, 64, D, 4), (D, 64, D, 4)) and refused((0, 64, D, 4), (8, 64, D, 4))
+    assert refused((0, 64, D, 4), (64, 64, D, 4)) and refused((0, 64, D, 4), (0, 80, D, 4))
+    # q_out against k, k_out against q, and both outputs; q of 4 heads and k of 2 in rows of 8 heads
+    q, k, free = (0, 128, D, 4), (64, 128, D, 2), (96, 128, D, 2)
+    assert refused(q, (48, 128, D, 4), k, free)               # over q's last head and k
+    assert refused((far, 128, D, 4), (32, 128, D, 4), k, free)
+    assert refused(q, q, k, (48, 128, D, 2)) and refused(q, q, k, (63, 128, D, 2)) and refused(q, q, q, q)
+    assert refused(q, (far, 128, D, 4), k, (far + 63, 128, D, 2))
+    assert refused((0, 64, D, 4), (far, 64, D, 4), (far + far, 64, D, 4), (far + 128, 64, D, 4))   # a token on
+    assert refused(q, (far, 128, D, 4), k, (far + 64, 64, D, 2))                # other token stride, spans meet
+    # in place, between one another, beside their inputs, head by head, other strides at a single token
+    for args in ((q, q, k, k), (q, (far, 128, D, 4), k, (far + 64, 128, D, 2)), (q, q, k, free),
+                 (q, (64, 128, D, 4)), ((0, 64, D, 2), (far, 48, 32, 2)), ((0, 4 * D, D, 4), (far, D, T * D, 4)),
+                 ((0, 96, 32, 3), (16, 96, 32, 3)), (q, q, (128 * T, 64, D, 2), (128 * T, 64, D, 2))):
+        assert call(*args, pos=None) == E.CONVROT_ERR_NULL, args
+    assert call(q, (0, 999, D, 4), T=1, pos=None) == E.CONVROT_ERR_NULL         # one token has no stride
+
+
+def test_rotary_binding_takes_views_beside_their_input():
+    pos, inv = z((3,), i64), z((8,), f32)
+    store = z((3, 12, 16))
+    for q, q_out in ((store[:, :4], store[:, 4:8]), (store[:, 4:8], store[:, :4]), (store[:, ::2], store[:, 1::2]),
+                     (store[:2, :4], store[1:, 8:]), (store.view(9, 4, 16)[:3], store.view(9, 4, 16)[3:6]),
+                     (store[:, :1].transpose(0, 1)[:, :1], store[:1, :1])):
+        _reaches_device(cr.convrot_rotary, q, None, pos[:q.shape[0]], inv, q_out=q_out)
+    flat = store.view(-1)
+    odd = lambda at, t, h, n: flat[at:].as_strided((3, n, 16), (t, h, 1))  # noqa: E731
+    for q, q_out in ((store[:, :4], store[:, 3:7]), (store[:2, 4:8], store[1:, 4:8]), (store[:, :4], odd(64, 96, 16, 4)),
+                     (odd(0, 192, 32, 4), odd(24, 192, 32, 4))):
+        _raises(cr.convrot_rotary, q, None, pos[:q.shape[0]], inv, q_out=q_out, match="overlaps")

@@ -164,3 +164,25 @@ def test_rotary_far_positions_keep_their_accuracy(cr, top, interleaved):
     off = (y.cpu().double() - ref).abs()
     tol = _bound(x, ref, R, interleaved, 1.0)
     assert bool((off <= tol).all()), f"worst {(off / tol).max().item():.3g} of the tolerance"
+
+
+def test_rotary_outputs_beside_inputs_and_over_others(cr):
+    """Outputs as views beside their inputs are right and leave the rest; over another tensor of the call they are
+    refused before anything is launched."""
+    print("\n[case] rotary outputs beside inputs", flush=True)
+    gen = torch.Generator().manual_seed(4)
+    T, D = 7, 32
+    store = torch.randn((T, 12, D), generator=gen).to(torch.bfloat16)
+    dev, pos, inv = store.to(DEV), torch.arange(T) * 37, cr.convrot_rotary_frequencies(D)
+    dpos, dinv = pos.to(DEV), inv.to(DEV)
+    q, k, q_out, k_out = dev.split((4, 2, 4, 2), dim=1)
+    for outs in ({"q_out": dev[:, 2:6]}, {"q_out": dev[:, 5:9]}, {"k_out": dev[:, 3:5]}, {"q_out": q_out, "k_out": dev[:, 9:11]},
+                 {"q_out": q, "k_out": q[:, :2]}):
+        with pytest.raises((cr.ConvRotError, ValueError)):
+            cr.convrot_rotary(q, k, dpos, dinv, **outs)
+        torch.cuda.synchronize()
+        assert torch.equal(dev.cpu(), store)
+    cr.convrot_rotary(q, k, dpos, dinv, q_out=q_out, k_out=k_out)
+    _check(q_out, store[:, :4], pos, inv, False)
+    _check(k_out, store[:, 4:6], pos, inv, False)
+    assert torch.equal(dev[:, :6].cpu(), store[:, :6])
