@@ -64,17 +64,21 @@ ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "bands": 3}
 
 
 # ------------------------------------------------------------------ linear, group scales
-@functools.lru_cache(maxsize=1024)
+# The library's answers for sizes as plain integers (a tensor as a key would stand for itself, not its value).
+@functools.lru_cache(maxsize=4096)
+def _size(name: str, *sizes: int) -> int:
+    return int(getattr(load_library(), name)(*sizes))
+
+
 def convrot_w4a16_padded_k(K: int, g: int, sg: int) -> int:
-    r = int(load_library().convrot_w4a16_padded_k(int(K), int(g), int(sg)))
+    r = _size("convrot_w4a16_padded_k", int(K), int(g), int(sg))
     if r < 0:
         _check(r, g)
     return r
 
 
-@functools.lru_cache(maxsize=4096)
 def convrot_w4a16_workspace_bytes(M: int, N: int, K: int, g: int, sg: int) -> int:
-    return int(load_library().convrot_w4a16_workspace_bytes(int(M), int(N), int(K), int(g), int(sg)))
+    return _size("convrot_w4a16_workspace_bytes", int(M), int(N), int(K), int(g), int(sg))
 
 
 def convrot_quant_weight_g4(w: torch.Tensor, g: int, sg: int, wq: Optional[torch.Tensor] = None,
@@ -316,11 +320,10 @@ def convrot_kv8_read(cu: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, 
     return k, v
 
 
-@functools.lru_cache(maxsize=4096)
 def convrot_kv8_attention_workspace_bytes(T: int, B: int, Hq: int, H: int, D: int, max_new: int,
                                           max_len: int) -> int:
-    return int(load_library().convrot_kv8_attention_workspace_bytes(
-        int(T), int(B), int(Hq), int(H), int(D), int(max_new), int(max_len)))
+    return _size("convrot_kv8_attention_workspace_bytes", int(T), int(B), int(Hq), int(H), int(D), int(max_new),
+                 int(max_len))
 
 
 def convrot_kv8_attention(q: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,

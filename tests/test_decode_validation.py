@@ -313,3 +313,19 @@ def test_rotary_binding_takes_views_beside_their_input():
     for q, q_out in ((store[:, :4], store[:, 3:7]), (store[:2, 4:8], store[1:, 4:8]), (store[:, :4], odd(64, 96, 16, 4)),
                      (odd(0, 192, 32, 4), odd(24, 192, 32, 4))):
         _raises(cr.convrot_rotary, q, None, pos[:q.shape[0]], inv, q_out=q_out, match="overlaps")
+
+
+def test_sizes_that_change_in_place_are_read_again():
+    """A size held in a tensor that a program counts up: its answer is that of its value, not of the first call's."""
+    n = torch.tensor(100)
+    assert cr.convrot_kv8_attention_workspace_bytes(5, 2, 4, 2, 64, 1, n) == 0
+    n += 1 << 20
+    assert cr.convrot_kv8_attention_workspace_bytes(5, 2, 4, 2, 64, 1, n) > 0
+    M = torch.tensor(2)
+    assert cr.convrot_w4a16_workspace_bytes(M, 100, 1000, 16, 32) == 0
+    M += 18
+    assert cr.convrot_w4a16_workspace_bytes(M, 100, 1000, 16, 32) >= 20 * 1024 * 2
+    K = torch.tensor(100)
+    assert cr.convrot_w4a16_padded_k(K, 16, 128) == 128
+    K += 100
+    assert cr.convrot_w4a16_padded_k(K, 16, 128) == 256
