@@ -141,11 +141,11 @@ def convrot_rotary_frequencies(R: int, base: float = 10000.0, scaling: str = "pl
     "linear", "ntk" or "bands", for contexts `factor` times the original one."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {', '.join(ROPE_SCALINGS)}, got {scaling!r}")
-    out = (ctypes.c_float * max(int(R) // 2, 1))()
+    out = (ctypes.c_float * 512)()                         # the library takes R up to 1024
     _check(load_library().convrot_rotary_frequencies(int(R), float(base), ROPE_SCALINGS[scaling],
                                                      float(factor), float(original), float(low), float(high),
                                                      ctypes.addressof(out)))
-    return torch.tensor(list(out), dtype=torch.float32)
+    return torch.tensor(out[:int(R) // 2], dtype=torch.float32)
 
 
 def _heads(t: torch.Tensor, name: str) -> Tuple[int, int, int]:

@@ -329,3 +329,12 @@ def test_sizes_that_change_in_place_are_read_again():
     assert cr.convrot_w4a16_padded_k(K, 16, 128) == 128
     K += 100
     assert cr.convrot_w4a16_padded_k(K, 16, 128) == 256
+
+
+def test_rotary_frequencies_of_any_size_are_answered_or_refused():
+    for R in (2, 1024):
+        assert cr.convrot_rotary_frequencies(R).tolist()[0] == 1.0 and cr.convrot_rotary_frequencies(R).shape == (R // 2,)
+    for R in (-2, 1 << 40, (1 << 63) - 2):                  # no host memory is asked for what is refused
+        with pytest.raises(cr.ConvRotError) as e:
+            cr.convrot_rotary_frequencies(R)
+        assert e.value.status == E.CONVROT_ERR_SHAPE
