@@ -346,9 +346,11 @@ CONVROT_API int convrot_w4a4_linear_noalloc(const void* x, int32_t x_dtype, int6
  *   0 where s = 0; packing as for int4 above.
  *   y[m][n] = bf16( sum_j s[n][j] sum_{k in group j} code[n][k] xr[m][k] + bias[n] ),
  *   xr = x zero-padded to K' and rotated in windows of g, rounded to fp16 after an exact
- *   power-of-two scaling of every 256 values (relative 2^-11); all sums fp32.
+ *   power-of-two scaling of every 256 values (relative 2^-11, at the least an absolute 2^-39 sqrt(g)
+ *   of the largest |x| among them, or among a window of 1024); all sums fp32.
  *   A weight group that holds an Inf or a NaN (or overflows in the rotation) gets a NaN scale;
- *   an activation row that holds one gives a NaN output row.
+ *   an activation row that holds one gives a NaN output row.  The sums of a scaled unit (values up to
+ *   2^15) times the scales stay in fp32 for scales up to 2^100.
  * --------------------------------------------------------------------------------------- */
 
 /* K' of the group-scaled layer, or a negative status (GROUP, UNSUPPORTED, SHAPE). */
@@ -366,8 +368,9 @@ CONVROT_API int convrot_quant_weight_g4(const void* w, int32_t w_dtype, int64_t 
 CONVROT_API size_t convrot_w4a16_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t g, int64_t sg);
 
 /* The layer: x [M][ldx], ldx >= K (any alignment of the element type), y bf16 [M][N] (2-byte
- * aligned), bias bf16 [N] or NULL.  Made for M up to some 64 rows; more run too, 64 at a time
- * (M <= 4194240, M ceil(K'/1024) <= 67108860, N <= 134217712).  workspace 256-byte aligned, NULL
+ * aligned), bias bf16 [N] or NULL.  Made for M up to some 64 rows; more run too, 64 at a time, the
+ * weights read and decoded again for each 64: prompts run at about a third of the rate of a dense
+ * product (M <= 4194240, M ceil(K'/1024) <= 67108860, N <= 134217712).  workspace 256-byte aligned, NULL
  * where it needs 0 bytes.  M = 0 or N = 0 is a no-op.  Results do not depend on the run; rows do not depend on one another.
  * Errors: GROUP, UNSUPPORTED, SHAPE, NULL, DTYPE, ALIGN, WORKSPACE, HIP. */
 CONVROT_API int convrot_w4a16_linear(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx,
@@ -419,6 +422,7 @@ CONVROT_API int convrot_rotary(const void* q, int64_t q_t, int64_t q_h, void* q_
  *   cu [B+1]      the rows of sequence b among the call's T rows are cu[b] ... cu[b+1]-1;
  *   lens [B]      its length, those rows included: they are its last tokens;
  *   table [B][max_pages] (row stride table_ld): its pages in order.
+ * Sequences have rows of their own: cu does not descend, but for sequences that are to be skipped.
  * What does not fit is skipped, never followed: sequences whose rows are not within [0, T] (these rows
  * are then of no sequence), table entries outside [0, num_pages), tokens beyond max_pages pages; append
  * and read skip a sequence that has more rows than its length, and to attention its first rows

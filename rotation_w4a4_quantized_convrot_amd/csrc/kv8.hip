@@ -545,7 +545,9 @@ __device__ __forceinline__ void put(const AttentionArgs& a, int D, int64_t split
 // bytes are the bound: a block's keys are asked for as soon as the last block's are used, its values as
 // soon as those are.  40 ragged sequences of up to 12000 tokens, 64 / 8 heads of 128: 130 us (4.4 TB/s; a
 // plain read of as much reaches 6), where waves that end early are what is left; one sequence of 200000
-// tokens, 32 / 8 heads: 92 us (4.5 TB/s), join included; one of 300 tokens: 7.3 us.
+// tokens, 32 / 8 heads: 92 us (4.5 TB/s), join included; one of 300 tokens: 7.4 us.  Less to read is further
+// from that rate: 40 sequences with one cached head 27 us (2.7 TB/s), 20000 tokens of 8 heads of 256 27 us
+// (3.0 TB/s, one workgroup of four waves a compute unit), 5 to 6 us of each for the join.
 template <int DT>
 constexpr size_t few_rows_lds_bytes() {
   return size_t(4) * 16 * (DT + 4) * 4;
@@ -751,10 +753,10 @@ constexpr int kAhead = 6;      // operand reads from LDS that are ahead of their
 // A block is two phases of a wave, one of vector arithmetic (its weights) and one of matrix
 // instructions (its values' product, then the next block's scores) with the decoding of coming blocks
 // between them.  The two waves of a SIMD, w and w + 4, are kept one phase apart by a barrier after
-// each, so that the matrix cores work for one while the other has its weights computed (3x900 rows
-// over 6000 tokens: 261 us with the groups apart, 289 without; waves 2 i and 2 i + 1 apart, which share no
-// SIMD, 319); the matrix phase has the higher priority (248 against 261 us).  With phases counted
-// over both groups, waves 0-3 do the weights of block i in phase 2 i and its products in 2 i + 1, waves
+// each, so that the matrix cores work for one while the other has its weights computed; the matrix phase
+// has the higher priority.  3x900 rows over 6000 tokens, 32 / 8 heads of 128: 240 us; 262 with one priority,
+// 278 with the groups in step, 315 with waves 2 i and 2 i + 1 apart, which share no SIMD.  Heads of 256
+// (16 / 4; one tile of rows a wave) 264, 265, 265 and 379.  With phases counted over both groups, waves 0-3 do the weights of block i in phase 2 i and its products in 2 i + 1, waves
 // 4-7 one later: keys of block j are read in phases 2 j - 1 and 2 j, values in 2 j + 1 and 2 j + 2.  In its
 // product phase of block i a wave writes its part of the keys of block i + 2 and of the values of block
 // i + 1: two buffers each are enough, and four places for the page scales (read in phases 2 j - 1 to
@@ -937,7 +939,7 @@ __global__ __launch_bounds__(512) void many_rows_kernel(AttentionArgs a, Kv8Batc
           // its use, and the other work in pieces between them; the compiler keeps this order.  A loop for
           // each product: as one of 64 rounds (heads above 128) the compiler does not write it out, and
           // every array that it indexes moves to scratch memory (3x900 rows over 6000 tokens, 16 / 4
-          // heads of 256: 69 ms so, 261 us in two loops)
+          // heads of 256: 69 ms so, 264 us in two loops)
           const uint8_t* const values = value_lds + (i & 1) * kHalf;
           const uint8_t* const keys = key_lds + ((i + 1) & 1) * kHalf;
           half8 ring[kAhead];

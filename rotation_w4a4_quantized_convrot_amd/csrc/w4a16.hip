@@ -6,7 +6,7 @@
 //
 // xr = x rotated in windows of g by H_g / sqrt(g) (g = 0: x itself).
 //
-// The weights are the traffic: N K'/2 bytes of codes, each read once.  The products run on
+// The weights are the traffic: N K'/2 bytes of codes, each read once for every 64 rows.  The products run on
 // v_mfma_f32_16x16x32_f16 with the codes exact in fp16 and the activations rounded to fp16
 // after an exact power-of-two scaling per unit of 256 values (decode_device.h, half_range): a
 // rounding of 2^-11 relative to each value, eight times finer than bf16's, where the output is
@@ -222,9 +222,10 @@ struct Load {
 // rows' first halves and columns 8-15 their second, against activation rows 0-7 and 8-15; the
 // two quadrants where they meet are the result.
 //
-// 5 x 4100 to 4111 (fp32, groups of 32): 8.7 us, a load's way to memory for each of a wave's two units;
-// 32 x 12288 to 4096: 26.3 us, 122 TFLOP/s: 128 workgroups, each of which reads the whole operand (0.8 MB)
-// from its L2, and nothing asked for ahead of its use.
+// 5 x 4100 to 4111 (fp32, groups of 32): 8.3 us, a load's way to memory for each of a wave's two units.
+// 8192 to 28672: 16 rows 51.5 us, 32 rows 66, 64 rows 97, 512 rows 547 (activations included): nothing is asked
+// for ahead of its use, every workgroup reads the whole operand (1 MB for 64 rows) from its L2, and
+// from 65 rows on the weights are read and decoded again for every 64.
 template <int MB, bool FOLD, int NT, int GC>
 __global__ __launch_bounds__(kWaves * 64) void product_kernel(
     Weights w, const _Float16* __restrict__ op, const float* __restrict__ factor, int64_t rows_padded,
@@ -301,9 +302,11 @@ __global__ __launch_bounds__(kWaves * 64) void product_kernel(
 
 // The product for prepared activations where tiles of 32 weight rows are too few for the chip: one tile of
 // 16, the waves' parts of K in steps of one load (128 columns), and what the next step needs asked for as
-// soon as this one has used the same registers.  32 x 12288 to 4096: 21 us with the activations' launch, 32
-// in product_kernel's tiles, which leave half the compute units idle.  Where there are enough of those
-// the operand, read once a tile, decides instead: 64 x 8192 to 28672 takes 128 us so, 80 in tiles of 64 rows.
+// soon as this one has used the same registers.  With the activations' launch, here and in product_kernel's
+// tiles of 32, which leave half the compute units idle: 32 x 12288 to 4096 22.6 and 32.3 us, 16, 32 and 64 rows
+// of 4096 to 4096 8.8 and 11.6, 10.4 and 14.6, 14.2 and 16.5.  Where there are enough of those the operand,
+// read once a tile, decides instead: 16, 32 and 64 rows of 8192 to 28672 take 60.6, 82 and 126 us so, 55, 69
+// and 100 in tiles of 32.
 template <int MB, typename G>
 __global__ __launch_bounds__(kWaves * 64, 2) void narrow_kernel(Weights w, const _Float16* __restrict__ op,
                                                                 const float* __restrict__ factor,
@@ -373,8 +376,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void narrow_kernel(Weights w, const
 // The weights' bytes bound it.  1 x 8192 to 28672 (121 MB): 28.5 us, 4.2 TB/s, where a plain read of as
 // much reaches 5.5; 35.7 us with x rotated again for every tile (long_vector_kernel).  One workgroup a
 // compute unit with 256 registers a lane: in an earlier form 35.9 us so and 40.7 with two workgroups of 128
-// registers, which do not hold the loads.  1 x 4096 to 4096: 6.2 us; 1 x 1024 to 1024: 4.6 us, of which the
-// launch is most.
+// registers, which do not hold the loads.  1 x 4096 to 4096: 6.3 us; 1 x 1024 to 1024: 5.0 us, of which the
+// launch is most.  Groups of 32 have four scales a load, and from K' = 4097 on their registers spill: 1 x 8192 to
+// 28672 takes 38.5 us, 1 x 16384 to 4096 27.8 (groups of 128: 13.3).
 template <int U>
 __host__ __device__ constexpr size_t vector_lds_bytes(int M) {
   return size_t(kWaves) * M * U * (2 * 136 * 2 + 4);      // a unit's halves 16 bytes apart in the banks
@@ -483,7 +487,8 @@ __global__ __launch_bounds__(kWaves * 64, U >= 2 ? 2 : 4) void vector_kernel(
 }
 
 // One launch for one or two rows that are longer: as above, but a wave goes through its part of K four
-// units at a time, for one tile, so that x is rotated again for every tile (1 x 8192 to 28672: 35.7 us).
+// units at a time, for one tile, so that x is rotated again for every tile.  1 x 28672 to 8192 (121 MB): 35 us,
+// 3.4 TB/s.
 template <typename TIn, int NT, int GC>
 __global__ __launch_bounds__(kWaves * 64) void long_vector_kernel(
     Weights w, const TIn* __restrict__ x, int M, int64_t K, int64_t ldx, bool wide, int digits, int64_t units,
@@ -567,7 +572,8 @@ __global__ __launch_bounds__(kWaves * 64) void long_vector_kernel(
 }
 
 // Weights, offline: rotate, one scale bf16(max / 7) per group, codes clamp(rne(value / scale)).  The
-// scale is rounded before the codes are taken, so that they are right for the scale that is kept.
+// scale is rounded before the codes are taken, so that they are right for the scale that is kept.  28672 x 8192
+// in bf16: 208 us, 2.8 TB/s, once for a model.
 template <typename TIn>
 __global__ __launch_bounds__(256) void quant_weight_kernel(const TIn* __restrict__ w, int64_t N, int64_t K,
                                                            bool wide, int digits, int64_t Kp, int sg,
