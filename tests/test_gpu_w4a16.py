@@ -221,3 +221,22 @@ def test_linear_graph_replays_and_streams(cr, M):
             assert torch.equal(y, e), f"replay {rep}"
         cr.convrot_w4a16_linear(x, g, sg, wq, ws, bias)
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("M,K,g,sg", [(2, 16384, 1024, 64), (2, 20000, 256, 128), (7, 4100, 64, 32), (65, 2048, 0, 64)])
+def test_linear_first_called_in_a_graph(cr, M, K, g, sg):
+    """Kernels that ask for more than 64 KB of LDS, or take a workspace, first called inside a capture; x changes
+    between the replays."""
+    print(f"\n[case] w4a16 graph first M={M} K={K} g={g} sg={sg}", flush=True)
+    x, wq, ws, bias = (t.to(DEV) for t in _inputs(M, K, 300, g, sg, torch.float32, K + 1, cr))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = cr.convrot_w4a16_linear(x, g, sg, wq, ws, bias)
+    for step in range(3):
+        x.copy_(x.flip(0) * (step + 1) + 0.25)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = cr.convrot_w4a16_linear(x, g, sg, wq, ws, bias)
+        assert torch.equal(y.view(torch.int16), want.view(torch.int16)), step
+        _check(y, x, g, wq, ws, bias)
