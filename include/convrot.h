@@ -346,8 +346,8 @@ CONVROT_API int convrot_w4a4_linear_noalloc(const void* x, int32_t x_dtype, int6
  *   0 where s = 0; packing as for int4 above.
  *   y[m][n] = bf16( sum_j s[n][j] sum_{k in group j} code[n][k] xr[m][k] + bias[n] ),
  *   xr = x zero-padded to K' and rotated in windows of g, rounded to fp16 after an exact
- *   power-of-two scaling of every 256 values (relative 2^-11, at the least an absolute 2^-39 sqrt(g)
- *   of the largest |x| among them, or among a window of 1024); all sums fp32.
+ *   power-of-two scaling of every 256 values (relative 2^-11, at the least an absolute 2^-39
+ *   sqrt(max(g, 1)) of the largest |x| among them, or among a window of 1024); all sums fp32.
  *   A weight group that holds an Inf or a NaN (or overflows in the rotation) gets a NaN scale;
  *   an activation row that holds one gives a NaN output row.  The sums of a scaled unit (values up to
  *   2^15) times the scales stay in fp32 for scales up to 2^100.

@@ -646,3 +646,23 @@ def test_attention_of_large_workgroups_in_a_graph(cr, lens, new, Hq, H, D):
         want = cr.convrot_kv8_attention(dq, dcu, dln, dt, *dc, max_new=max(new), max_len=max(lens))
         assert torch.equal(out, want), step
         check_attention(out, q, cum(new), dln.cpu(), table, cache, 0, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("rows,D,G", [(1, 64, 4), (8, 128, 8), (60, 64, 2), (70, 256, 1)])
+@pytest.mark.parametrize("low,high", [(-50, 50), (-79, 21), (0, 100)])
+def test_attention_value_scales_far_apart(cr, rows, D, G, low, high):
+    """Value scales 2^100 apart: tokens of the small ones still count in the sum, first, in between or last, one
+    share or several."""
+    print(f"\n[case] attention value scales 2^{low} and 2^{high} rows={rows} D={D}", flush=True)
+    gen = torch.Generator().manual_seed(rows + high)
+    length = 150 + rows
+    table, pages = paging([length], 16, gen)
+    cu, ln = cum([rows]), torch.tensor([length], dtype=torch.int32)
+    q = torch.randn((rows, G, D), generator=gen).to(torch.bfloat16)
+    for large in ([0], [4], [8], [0, 3, 6], [1, 2, 3, 4, 5, 7, 8]):
+        cache = cache_of(pages, 1, 16, D, gen)
+        cache[3].fill_(2.0 ** low)
+        cache[3][table[0, large].long()] = 2.0 ** high
+        for max_len in (1, 4000):
+            out = cr.convrot_kv8_attention(q.to(DEV), cu.to(DEV), ln.to(DEV), table.to(DEV), *to(cache), max_len=max_len)
+            check_attention(out, q, cu, ln, table, cache, 0, 1 / math.sqrt(D))

@@ -240,3 +240,16 @@ def test_linear_first_called_in_a_graph(cr, M, K, g, sg):
         want = cr.convrot_w4a16_linear(x, g, sg, wq, ws, bias)
         assert torch.equal(y.view(torch.int16), want.view(torch.int16)), step
         _check(y, x, g, wq, ws, bias)
+
+
+@pytest.mark.parametrize("M", [1, 2, 6, 20, 70])
+@pytest.mark.parametrize("log_scale,log_x", [(100, -110), (100, 0), (-100, 90), (-126, 100)])
+def test_linear_scales_at_the_limits(cr, M, log_scale, log_x):
+    """Scales up to 2^100, with values that bring the products back into range, and tiny ones."""
+    print(f"\n[case] w4a16 scales M={M} 2^{log_scale} x 2^{log_x}", flush=True)
+    K, N, g, sg = 600, 40, 64, 32
+    x, wq, ws, _ = _inputs(M, K, N, g, sg, torch.float32, 11, cr)
+    x *= 2.0 ** log_x
+    ws = (1 + ws * 50).to(torch.bfloat16).float().clamp(max=1.9) * 2.0 ** (log_scale - 1)
+    ws = ws.to(torch.bfloat16)
+    _check(cr.convrot_w4a16_linear(x.to(DEV), g, sg, wq.to(DEV), ws.to(DEV)), x, g, wq, ws, None)
