@@ -294,7 +294,8 @@ def convrot_kv8_read(cu: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, 
                      tokens: Optional[int] = None, max_new: Optional[int] = None,
                      k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None):
     """The last cu[b+1] - cu[b] tokens of each sequence -> (k, v) bf16 [tokens, H, D].  tokens: cu's
-    last element, which stays on the device; not needed with k and v given."""
+    last element, which stays on the device; not needed with k and v given.  Rows of no sequence are left
+    as they were: undefined in new tensors."""
     B, batch = _batch(cu, lens, table)
     H, page, D, cache = _cache(kc, ks, vc, vs, g)
     for t, name in ((k, "k"), (v, "v")):
@@ -333,7 +334,8 @@ def convrot_kv8_attention(q: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor,
                           workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """q [T, Hq, D] (bf16/fp32, strided), whose keys and values are in the cache already -> out bf16
     [T, Hq, D].  scale: 1/sqrt(D) by default.  max_new, max_len: the largest row count and length of a
-    sequence (default: T and what the table holds); they size the launch and the workspace only."""
+    sequence (default: T and what the table holds); they size the launch and the workspace only.  Rows of no
+    sequence are left as they were: undefined in a new tensor."""
     T, Hq, D = _heads(q, "q")
     B, batch = _batch(cu, lens, table)
     H, page, cD, cache = _cache(kc, ks, vc, vs, g)
@@ -449,7 +451,7 @@ class ConvAttention(torch.nn.Module):
     def forward(self, x: torch.Tensor, pos: torch.Tensor, cache: KVCache8bit, cu: torch.Tensor, lens: torch.Tensor,
                 table: torch.Tensor, max_new: Optional[int] = None, max_len: Optional[int] = None) -> torch.Tensor:
         """x [T, features]: the new tokens' rows of all sequences, pos int64 [T] their positions; the cache
-        gets their keys and values."""
+        gets their keys and values.  Rows of no sequence (a padded batch) come out undefined."""
         T = x.shape[0]
         rows = self.qkv(x).view(T, self.heads + 2 * self.kv_heads, self.head_dim)
         q, k, v = rows.split((self.heads, self.kv_heads, self.kv_heads), dim=1)
