@@ -560,7 +560,8 @@ CONVROT_API int convrot_kv8_copy(const int32_t* src, const int32_t* dst, int64_t
  * x [M][K] of x_dtype (row stride ldx); a bf16 [L][r][K], b bf16 [L][N][r], scale fp32 [L]: adapters of lower rank
  * are padded with zeros; y and out bf16 [M][N] (row strides ldy, ldo); ids int32 [M], a row whose id is outside
  * [0, L) has no adapter: its y is copied.  Pointers aligned to their elements.  Sums are fp32; an fp32 x, and
- * h, enter the products as two bf16 pieces each, 2^-16 relative.
+ * h, enter the products as two bf16 pieces each, 2^-16 relative (below 2^-133 an absolute 2^-134).  Inf and NaN go through as
+ * the formula has them.
  * out is y (the same pointer and row stride) or overlaps neither y nor x.  M = 0 or N = 0 is a no-op.
  * 1 <= L <= 2^24, 1 <= r <= 256, M <= 4194240.  workspace 256-byte aligned.  Results do not depend on the run; rows do not
  * depend on one another.  Errors: DTYPE, SHAPE, UNSUPPORTED, NULL, ALIGN, WORKSPACE, HIP. */

@@ -4,8 +4,8 @@
 //
 // h first, in fp32, split over K into partial sums that the second launch adds up in their order.  Both
 // products run on v_mfma_f32_16x16x32_bf16; A and B are bf16 already, fp32 operands (x where it is fp32, and h)
-// enter as two bf16 pieces, the value cut off and its rest: 2^-16 relative.  A row's sums do not depend on the
-// rows beside it, nor on its place in a tile.
+// enter as two bf16 pieces, the value cut off and its rest: 2^-16 relative, below 2^-133 an absolute 2^-134.  A
+// row's sums do not depend on the rows beside it, nor on its place in a tile.
 //
 // Few rows: a workgroup to each row of a tile of 16, of which the first with its adapter goes on, for all rows
 // of the tile that have it; operands go straight into registers.  Many rows: the rows are sorted by adapter
@@ -19,6 +19,7 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint16_t ushort8 __attribute__((ext_vector_type(8)));
+typedef int16_t short8 __attribute__((ext_vector_type(8)));
 typedef float float8 __attribute__((ext_vector_type(8)));
 
 constexpr int kWaves = 4;
@@ -37,6 +38,14 @@ __device__ __forceinline__ uint16_t cut(float v) {
 __device__ __forceinline__ float rest(float v) {
   const uint32_t u = __float_as_uint(v);
   return (u & 0x7F800000u) == 0x7F800000u ? 0.0f : v - __uint_as_float(u & 0xFFFF0000u);
+}
+
+// What a second piece is multiplied with: the values, but the largest finite ones in the place of Inf and NaN.  The first
+// piece makes the Inf or NaN of such a weight; a second piece of 0 would make a NaN of an Inf.  Its sign is the first one's, so
+// that its product agrees with the Inf even where it overflows.
+__device__ __forceinline__ bf16x8 finite(const bf16x8& v) {
+  const ushort8 below = __builtin_elementwise_min(__builtin_bit_cast(ushort8, v), ushort8(0xFF7F));       // negative ones
+  return __builtin_bit_cast(bf16x8, __builtin_elementwise_min(__builtin_bit_cast(short8, below), short8(0x7F7F)));
 }
 
 // Eight neighbouring elements as they stand in memory.  Rows need no alignment beyond their elements'.
@@ -149,7 +158,7 @@ __global__ __launch_bounds__(kWaves * 64) void few_shrink_kernel(LoraArgs a) {
       for (int rt = 0; rt < RT; ++rt) {
         const Operand ws(s.w[rt][i]);
         sum[rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xs.high, ws.high, sum[rt], 0, 0, 0);
-        if (sizeof(TIn) == 4) sum[rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xs.low, ws.high, sum[rt], 0, 0, 0);
+        if (sizeof(TIn) == 4) sum[rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xs.low, finite(ws.high), sum[rt], 0, 0, 0);
       }
     }
   };
@@ -261,7 +270,7 @@ __global__ __launch_bounds__(kWaves * 64) void few_expand_kernel(LoraArgs a, int
       for (int t = 0; t < 4; ++t) {
         const Operand bs(s.b[t][ks]);
         sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bs.high, h.high, sum[t], 0, 0, 0);
-        sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bs.high, h.low, sum[t], 0, 0, 0);
+        sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(finite(bs.high), h.low, sum[t], 0, 0, 0);
       }
     }
     const int64_t col = n0 + 16 * c, there = a.N - col;
@@ -472,7 +481,7 @@ __global__ __launch_bounds__(kWaves * 64) void many_shrink_kernel(LoraArgs a) {
       for (int rt = 0; rt < RT; ++rt) {
         const bf16x8 u = *reinterpret_cast<const bf16x8*>(&a_lds[buffer][(rt * 16 + n) * kStride + at]);
 #pragma unroll
-        for (int p = 0; p < kPieces; ++p) sum[rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[p], u, sum[rt], 0, 0, 0);
+        for (int p = 0; p < kPieces; ++p) sum[rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[p], p == 0 ? u : finite(u), sum[rt], 0, 0, 0);
       }
     }
   }
@@ -611,7 +620,7 @@ __global__ __launch_bounds__(kWaves * 64) void many_expand_kernel(LoraArgs a, in
         for (int ks = 0; ks < KS; ++ks) {
           const bf16x8 b = *reinterpret_cast<const bf16x8*>(&b_lds[(64 * half + 16 * t + n) * kStride + 32 * ks + 8 * c]);
           sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, high[ks], sum, 0, 0, 0);
-          sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, low[ks], sum, 0, 0, 0);
+          sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(finite(b), low[ks], sum, 0, 0, 0);
         }
         *reinterpret_cast<float4_t*>(&sum_lds[n * 68 + 16 * t + 4 * c]) = sum;     // columns x rows: 4 columns of row n
       }

@@ -212,3 +212,36 @@ def test_empty(cr):
     for M, N in ((0, 5), (5, 0)):
         args = on(inputs(M, 8, N, 4, 2, torch.bfloat16, 1))
         assert cr.convrot_lora(*args).shape == (M, N)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,K,N,r", [(5, 64, 40, 8), (40, 200, 70, 64), (20, 128, 33, 200), (90, 96, 130, 24), (150, 300, 50, 256)])
+def test_infinite_weights(cr, M, K, N, r, dtype):
+    """An Inf in a or b makes +-Inf, or NaN beside a 0 or an Inf of the other sign, as the formula does; values that are
+    exact in bf16, whose second piece is 0, and values that are not."""
+    print(f"\n[case] lora infinite weights M={M} K={K} N={N} r={r} {dtype}", flush=True)
+    inf = float("inf")
+    for exact in (True, False):
+        args = inputs(M, K, N, r, 3, dtype, M + r)
+        x, ids, a, b, scale, y = args
+        ids[:] = torch.arange(M, dtype=torch.int32) % 4 - 1
+        if exact:                                                # h_j = 2 x_j: whole numbers, some of them 0
+            a[:] = 0
+            a[:, torch.arange(r), torch.arange(r) % K] = 2.0
+            x.copy_((x * 2).round().clamp(-3, 3))
+        scale[:] = torch.tensor([0.5, -1.0, 2.0])
+        b[0, 3, 1], b[0, 7, 2], b[0, 9, 1], b[0, 9, 3] = inf, -inf, inf, -inf
+        b[1, N - 1, r - 1] = -inf
+        if not exact:
+            a[2, 4, K - 1], a[2, 5, 3] = inf, -inf
+        h = (a[ids.long().clamp(min=0)].double() * x.double()[:, None]).sum(-1)
+        add = scale.double()[ids.long().clamp(min=0), None] * (b[ids.long().clamp(min=0)].double() * h[:, None]).sum(-1)
+        ref = y.double() + torch.where((ids >= 0)[:, None], add, torch.zeros_like(add))
+        out = cr.convrot_lora(*on(args)).cpu().double()
+        assert bool(ref.isinf().any()) and bool(ref.isfinite().any())
+        assert torch.equal(out.isnan(), ref.isnan())
+        assert torch.equal(out[ref.isinf()], ref[ref.isinf()])
+        good = ref.isfinite()
+        size = O.lora(x, ids, a.nan_to_num(0, 0, 0), b.nan_to_num(0, 0, 0), scale, y)[1]
+        tol = size * (2 * 2.0 ** -16 + (K + 2 * r + 64) * 2.0 ** -24 + 2.0 ** -23) + 2.0 ** -8 * ref.abs()
+        assert bool(((out - ref).abs() <= tol)[good].all())
