@@ -518,7 +518,9 @@ CONVROT_API size_t convrot_kv8_tree_attention_workspace_bytes(int64_t T, int64_t
 /* convrot_kv8_attention in which a row sees all tokens before its sequence's rows, and of those rows' own tokens
  * (in the cache already: row j's is token lens[b] - n + j) the ones whose bits its words of the mask [T][words]
  * set; any mask will do.  Rows whose sequence has no earlier tokens and whose mask is empty are zero.  All else,
- * limits and roundings included, as for convrot_kv8_attention.  words 1 to 1024, mask 8-byte aligned.
+ * limits and roundings included, as for convrot_kv8_attention, but that T Hq is below 2^28 for D up to 64, 2^27 up to
+ * 128 and 2^26 above where a cached head is to have more than 64 rows (max_new Hq / H).  words 1 to 1024, mask 8-byte
+ * aligned.
  * Errors: GROUP, UNSUPPORTED, SHAPE, NULL, DTYPE, ALIGN, WORKSPACE, HIP. */
 CONVROT_API int convrot_kv8_tree_attention(const void* q, int64_t q_t, int64_t q_h, int32_t dtype, int64_t T,
                                            int64_t Hq, const uint64_t* mask, int64_t words, const int32_t* cu,

@@ -67,7 +67,8 @@ size_t attention_workspace(decltype(convrot::plan_kv8_attention)* plan_of, int64
   if (!attention_shape_ok(T, B, Hq, H, D, max_new, max_len) || !attention_plannable(T, B, Hq, H) || T == 0 ||
       B == 0 || D > 256 || D % 16 != 0)
     return 0;
-  return plan_of(B, T, Hq, H, D, max_new, max_len).bytes;
+  const convrot::Kv8Plan p = plan_of(B, T, Hq, H, D, max_new, max_len);
+  return p.threads <= kMaxThreads ? p.bytes : 0;
 }
 
 // What the entry points for attention over the cache refuse, and the plan of a call; *nothing: there is nothing to do.
@@ -86,10 +87,7 @@ int check_attention(const void* q, int64_t q_t, int64_t q_h, int32_t dtype, int6
   if (*nothing) return CONVROT_OK;
   if (!attention_plannable(T, B, Hq, H)) return CONVROT_ERR_UNSUPPORTED;
   const convrot::Kv8Plan plan = *p = plan_of(B, T, Hq, H, D, max_new, max_len);
-  // workgroups of 256 threads for few rows, 512 for many; joining the splits takes one to a row at most
-  if (plan.row_blocks > kMaxThreads / (plan.row_tiles <= 4 ? 256 : 512) / plan.splits / H / B ||
-      (plan.splits > 1 && !launch_fits(T * Hq, 256)))
-    return CONVROT_ERR_UNSUPPORTED;
+  if (plan.threads > kMaxThreads) return CONVROT_ERR_UNSUPPORTED;
   if (q == nullptr || out == nullptr || (plan.bytes > 0 && workspace == nullptr)) return CONVROT_ERR_NULL;
   st = check_batch_pointers(cu, lens, table, max_pages, kc, ks, vc, vs);
   if (st != CONVROT_OK) return st;

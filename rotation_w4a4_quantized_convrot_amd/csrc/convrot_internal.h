@@ -138,6 +138,7 @@ struct Kv8Plan {
   int64_t row_blocks;  // per sequence and cached head
   int splits;          // of a sequence's tokens
   size_t bytes;
+  int64_t threads;     // of its largest launch
 };
 Kv8Plan plan_kv8_attention(int64_t B, int64_t T, int64_t Hq, int64_t H, int64_t D, int64_t max_new,
                            int64_t max_len);

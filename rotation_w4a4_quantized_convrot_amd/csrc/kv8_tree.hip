@@ -318,6 +318,8 @@ Kv8Plan plan_kv8_tree(int64_t B, int64_t T, int64_t Hq, int64_t H, int64_t D, in
   const int64_t groups = B * H * p.row_blocks;
   p.splits = int(2 + 2 * std::min<int64_t>(ceil_div(kParts, groups), ceil_div(blocks, kShare)));
   p.bytes = round256(size_t(p.splits) * T * Hq * D * 4) + round256(size_t(p.splits) * T * Hq * 8);
+  const int lanes = join_lanes(int(D));
+  p.threads = std::max<int64_t>(kParts * 512, ceil_div(T * Hq, 256 / lanes) * 256);
   return p;
 }
 

@@ -191,3 +191,19 @@ def test_attention_block_arguments():
     assert "q_norm" not in cr.ConvAttention(lin(64, 4 * 32), lin(64, 64), 2, 1, inv).state_dict()
     _raises(cr.ConvAttention, lin(64, 4 * 32), lin(64, 64), 2, 1, inv, q_norm=torch.ones(32), match="together")
     _raises(cr.ConvAttention, lin(64, 4 * 32), lin(64, 64), 2, 1, inv, q_norm=torch.ones(32), k_norm=torch.ones(31), match="k_norm")
+
+
+def test_tree_attention_limits(lib):
+    """Many rows run on as many workgroups as the chip holds, however many blocks of rows there are; what the entry point
+    refuses has no workspace."""
+    def call(T, B, Hq, H, D, new, length, nbytes=0):
+        return lib.convrot_kv8_tree_attention(A, Hq * D, D, 1, T, Hq, A, 1, A, A, A, 4, B, 4, A, A, A, A, 10, 64, H, D, 0,
+                                              ctypes.c_float(1.0), new, length, A, A, nbytes, None)
+    size = cr.convrot_kv8_tree_attention_workspace_bytes
+    for args in ((30000, 300, 64, 8, 128, 30000, 8192), (30000, 300, 64, 8, 128, 100, 8192), (2 ** 19, 5, 64, 8, 128, 9, 100),
+                 (2 ** 21 - 1, 5, 64, 8, 128, 9, 100), (2 ** 22 - 1, 5, 64, 8, 64, 9, 100), (2 ** 20 - 1, 5, 64, 8, 256, 9, 100)):
+        assert size(*args) > 0 and call(*args) == call(*args, size(*args) - 1) == E.CONVROT_ERR_WORKSPACE, args
+    for args in ((2 ** 21, 5, 64, 8, 128, 9, 100), (2 ** 22, 5, 64, 8, 64, 9, 100), (2 ** 20, 5, 64, 8, 256, 9, 100),
+                 (2 ** 20, 1, 32, 1, 64, 1, 100000)):
+        assert size(*args) == 0 and call(*args) == E.CONVROT_ERR_UNSUPPORTED, args
+    assert cr.convrot_kv8_attention_workspace_bytes(2 ** 20, 1, 32, 1, 64, 1, 100000) == 0

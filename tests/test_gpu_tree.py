@@ -449,3 +449,20 @@ def test_two_threads(cr):
     for t in threads:
         t.join()
     assert not wrong, wrong
+
+
+def test_many_trees_with_default_hints(cr):
+    """300 trees of 100 tokens, 64 / 8 heads, with no hint at how many a sequence has: some of them against the definition."""
+    print("\n[case] tree attention of 300 trees of 100, default hints", flush=True)
+    gen = torch.Generator().manual_seed(41)
+    B, n, Hq, H, D, page = 300, 100, 64, 8, 16, 32
+    lens = [n + int(torch.randint(0, 90, (1,), generator=gen)) for _ in range(B)]
+    table, pages = paging(lens, page, gen)
+    cache = cache_of(pages, H, page, D, gen)
+    q = torch.randn((B * n, Hq, D), generator=gen).to(torch.bfloat16)
+    mask = random_mask(B * n, 2, gen)
+    cu, ln = cum([n] * B), i32(lens)
+    out = cr.convrot_kv8_tree_attention(q.to(DEV), mask.to(DEV), cu.to(DEV), ln.to(DEV), table.to(DEV), *to(cache), g=16)
+    for b in (0, 1, 150, 298, 299):
+        at = slice(b * n, b * n + n)
+        check(out[at], q[at], mask[at], cum([n]), ln[b:b + 1], table[b:b + 1], cache, 16, 1 / math.sqrt(D))
