@@ -534,7 +534,7 @@ CONVROT_API int convrot_kv8_tree_attention(const void* q, int64_t q_t, int64_t q
  * `kept` lists stay and move together behind the tokens before them.  kept int32 [T]: for each sequence, from its
  * first row on, the rows that stay, counted from its first row and ascending; a list ends before its first entry
  * that is outside [0, n) or not above the one before it, or after n entries.
- *   lens_out int32 [B] (over no other tensor of the call; or NULL): lens[b] - n + the length of the list; lens[b] for sequences that
+ *   lens_out int32 [B] (over no other tensor of the call nor the workspace; or NULL): lens[b] - n + the length of the list; lens[b] for sequences that
  *     are skipped, or whose n is larger than lens[b].
  * A page that receives tokens gets as its scale the largest of those of the pages that its tokens come from, tokens
  * before it included; codes that come under a larger scale become rne(code * fp32(S_old / S)), others stay.  A

@@ -111,7 +111,12 @@ int convrot_kv8_keep(const int32_t* kept, int64_t T, const int32_t* cu, const in
                               !apart(lens_out, 4 * B, kept, 4 * T) ||
                               (max_pages > 0 && !apart(lens_out, 4 * B, table, bytes_of(B, max_pages, table_ld, 4)))))
     return CONVROT_ERR_SHAPE;
-  if (ws_bytes < convrot::kv8_keep_bytes(T, B, H, D)) return CONVROT_ERR_WORKSPACE;
+  const int64_t need = int64_t(convrot::kv8_keep_bytes(T, B, H, D)), codes = num_pages * H * page * D, scales = 4 * num_pages * H;
+  if (ws_bytes < size_t(need)) return CONVROT_ERR_WORKSPACE;
+  if (lens_out != nullptr && (!apart(lens_out, 4 * B, kc, codes) || !apart(lens_out, 4 * B, ks, scales) ||
+                              !apart(lens_out, 4 * B, vc, codes) || !apart(lens_out, 4 * B, vs, scales) ||
+                              !apart(lens_out, 4 * B, workspace, need)))
+    return CONVROT_ERR_SHAPE;
   const convrot::Kv8Batch batch{cu, lens, table, B, T, table_ld, max_pages};
   const convrot::Kv8Cache cache{kc, ks, vc, vs, num_pages, int(page), int(H), int(D)};
   return status_of(convrot::launch_kv8_keep(kept, batch, cache, max_new < T ? max_new : T, lens_out, workspace,

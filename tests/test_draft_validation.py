@@ -207,3 +207,20 @@ def test_tree_attention_limits(lib):
                  (2 ** 20, 1, 32, 1, 64, 1, 100000)):
         assert size(*args) == 0 and call(*args) == E.CONVROT_ERR_UNSUPPORTED, args
     assert cr.convrot_kv8_attention_workspace_bytes(2 ** 20, 1, 32, 1, 64, 1, 100000) == 0
+
+
+def test_keep_lengths_over_the_cache(lib):
+    """lens_out lies over none of the cache's tensors nor the workspace; beside them it passes on to the next check."""
+    P, H, page, D, T, B, far = 10, 2, 16, 64, 5, 2, 0x1000000
+    at = {"kc": (1, P * H * page * D), "ks": (2, 4 * P * H), "vc": (3, P * H * page * D), "vs": (4, 4 * P * H)}
+    need = cr.convrot_kv8_keep_workspace_bytes(T, B, H, D)
+    at["work"] = (5, need)
+
+    def call(out, **k):
+        p = {name: k.get(name, far * n) for name, (n, _) in at.items()}
+        return lib.convrot_kv8_keep(A, T, A + 0x100, A + 0x200, A + 0x300, 4, B, 4, p["kc"], p["ks"], p["vc"], p["vs"], P, page, H, D,
+                                    3, out, p["work"], need, None)
+    for name, (n, size) in at.items():
+        for out in (far * n, far * n + size - 4, far * n - 4):
+            assert call(out) == E.CONVROT_ERR_SHAPE, name
+    assert call(far * 5 + need - 4) == E.CONVROT_ERR_SHAPE
