@@ -564,7 +564,9 @@ CONVROT_API int convrot_kv8_copy(const int32_t* src, const int32_t* dst, int64_t
  * [0, L) has no adapter: its y is copied.  Pointers aligned to their elements.  Sums are fp32; an fp32 x, and
  * h, enter the products as two bf16 pieces each, 2^-16 relative (below 2^-133 an absolute 2^-134).  Inf and NaN go through as
  * the formula has them.
- * out is y (the same pointer and row stride) or overlaps neither y nor x.  M = 0 or N = 0 is a no-op.
+ * out is y (the same pointer and row stride), and else apart from every tensor of the call and from the workspace: from its
+ * first element to its last it reaches into none of theirs (SHAPE), also where views of one buffer lie between one
+ * another.  M = 0 or N = 0 is a no-op.
  * 1 <= L <= 2^24, 1 <= r <= 256, M <= 4194240.  workspace 256-byte aligned.  Results do not depend on the run; rows do not
  * depend on one another.  Errors: DTYPE, SHAPE, UNSUPPORTED, NULL, ALIGN, WORKSPACE, HIP. */
 CONVROT_API size_t convrot_lora_workspace_bytes(int64_t M, int64_t K, int64_t r, int64_t L);

@@ -167,7 +167,11 @@ int convrot_lora(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t l
   if (out == y ? M > 1 && ldy != ldo : !apart(out, bytes_of(M, N, ldo, 2), y, bytes_of(M, N, ldy, 2)))
     return CONVROT_ERR_SHAPE;
   if (!apart(out, bytes_of(M, N, ldo, 2), x, bytes_of(M, K, ldx, size))) return CONVROT_ERR_SHAPE;
-  if (ws_bytes < convrot_lora_workspace_bytes(M, K, r, L)) return CONVROT_ERR_WORKSPACE;
+  const int64_t need = int64_t(convrot_lora_workspace_bytes(M, K, r, L));
+  if (ws_bytes < size_t(need)) return CONVROT_ERR_WORKSPACE;
+  for (const auto& [other, bytes] : {std::pair<const void*, int64_t>{ids, 4 * M}, {a, 2 * L * r * K}, {b, 2 * L * N * r},
+                                     {scale, 4 * L}, {workspace, need}})
+    if (!apart(out, bytes_of(M, N, ldo, 2), other, bytes)) return CONVROT_ERR_SHAPE;
   convrot::LoraArgs args{};
   args.x = x;
   args.ldx = ldx;

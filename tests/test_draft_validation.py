@@ -224,3 +224,19 @@ def test_keep_lengths_over_the_cache(lib):
         for out in (far * n, far * n + size - 4, far * n - 4):
             assert call(out) == E.CONVROT_ERR_SHAPE, name
     assert call(far * 5 + need - 4) == E.CONVROT_ERR_SHAPE
+
+
+def test_lora_answers_over_other_tensors(lib):
+    """out lies over neither ids, the adapters, their scales nor the workspace."""
+    M, K, N, r, L, far = 5, 64, 32, 8, 2, 0x1000000
+    need = cr.convrot_lora_workspace_bytes(M, K, r, L)
+    size = {"ids": 4 * M, "a": 2 * L * r * K, "b": 2 * L * N * r, "scale": 4 * L, "work": need}
+    at = {name: far * (i + 1) for i, name in enumerate(size)}
+    mine = 2 * M * N
+
+    def call(out, y=far * 20):
+        return lib.convrot_lora(far * 21, 1, M, K, K, at["ids"], at["a"], at["b"], at["scale"], r, L, y, N, N, out, N, at["work"],
+                                need, None)
+    for name, n in size.items():
+        for out in (at[name], at[name] + n - 2, at[name] - mine + 2):
+            assert call(out) == call(out, out) == E.CONVROT_ERR_SHAPE, name
