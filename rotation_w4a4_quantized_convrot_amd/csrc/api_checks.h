@@ -4,6 +4,8 @@
 #include "convrot.h"
 #include "convrot_internal.h"
 
+#include <initializer_list>
+
 namespace {
 
 constexpr int64_t kIntMax = 0x7FFFFFFF;
@@ -151,6 +153,30 @@ struct TurnedPart {
   void* out;
   int64_t out_t, out_h, heads;
 };
+
+bool apart(const void* a, int64_t an, const void* b, int64_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x + uintptr_t(an) <= y || y + uintptr_t(bn) <= x;
+}
+
+// A tensor as bytes in memory.
+struct Extent {
+  const void* at;
+  int64_t bytes;
+};
+
+// Whether the tensors that are not turned (NULL: none) lie apart from what is written, from each output's first element to
+// its last.
+bool apart_from_outputs(const TurnedPart (&part)[2], int32_t dtype, int64_t T, int64_t D,
+                        std::initializer_list<Extent> others) {
+  for (const auto& p : part) {
+    if (p.heads == 0) continue;
+    const int64_t span = span_of(Rows{0, p.out_t, p.out_h, p.heads}, T, D) * int64_t(elem_size(dtype));
+    for (const Extent& o : others)
+      if (o.at != nullptr && !apart(p.out, span, o.at, o.bytes)) return false;
+  }
+  return true;
+}
 
 // What the entry points for rotary positions refuse; *nothing: there is nothing to do.
 int check_turned(const TurnedPart (&part)[2], int32_t dtype, int64_t T, int64_t D, int64_t R, const int64_t* pos,

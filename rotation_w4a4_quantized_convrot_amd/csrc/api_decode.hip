@@ -109,6 +109,7 @@ int convrot_rotary(const void* q, int64_t q_t, int64_t q_h, void* q_out, int64_t
   bool nothing = false;
   const int st = check_turned(part, dtype, T, D, R, pos, inv_freq, &nothing);
   if (st != CONVROT_OK || nothing) return st;
+  if (!apart_from_outputs(part, dtype, T, D, {{pos, 8 * T}, {inv_freq, 2 * R}})) return CONVROT_ERR_SHAPE;
   convrot::RotaryArgs a{{q, q_out, q_t, q_h, qo_t, qo_h, int(Hq)}, {k, k_out, k_t, k_h, ko_t, ko_h, int(Hk)},
                         pos, inv_freq, factor, int(D), int(R), interleaved != 0, inverse != 0};
   return status_of(convrot::launch_rotary(a, dtype, T, static_cast<hipStream_t>(stream)));

@@ -2,8 +2,6 @@
 // validation and launches.  Semantics: include/convrot.h.
 #include "api_checks.h"
 
-#include <utility>
-
 namespace {
 
 constexpr int64_t kMaxWords = 1024, kMaxAdapters = 1 << 24;
@@ -16,11 +14,6 @@ int check_lora(int64_t M, int64_t K, int64_t r, int64_t L) {
 
 // Bytes from a matrix' first element to behind its last; strides are within kMaxStride.
 int64_t bytes_of(int64_t rows, int64_t cols, int64_t ld, int64_t size) { return ((rows - 1) * ld + cols) * size; }
-
-bool apart(const void* a, int64_t an, const void* b, int64_t bn) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x + uintptr_t(an) <= y || y + uintptr_t(bn) <= x;
-}
 
 }  // namespace
 
@@ -38,6 +31,9 @@ int convrot_norm_rotary(const void* q, int64_t q_t, int64_t q_h, void* q_out, in
   const int st = check_turned(part, dtype, T, D, R, pos, inv_freq, &nothing);
   if (st != CONVROT_OK || nothing) return st;
   if (!aligned(q_weight, elem_size(w_dtype)) || !aligned(k_weight, elem_size(w_dtype))) return CONVROT_ERR_ALIGN;
+  const int64_t bytes = D * int64_t(elem_size(w_dtype));
+  if (!apart_from_outputs(part, dtype, T, D, {{pos, 8 * T}, {inv_freq, 2 * R}, {q_weight, bytes}, {k_weight, bytes}}))
+    return CONVROT_ERR_SHAPE;
   const convrot::NormRotaryArgs a{{{q, q_out, q_t, q_h, qo_t, qo_h, int(Hq)}, {k, k_out, k_t, k_h, ko_t, ko_h, int(Hk)},
                                    pos, inv_freq, factor, int(D), int(R), interleaved != 0, 0},
                                   q_weight, k_weight, w_dtype, eps};
@@ -52,7 +48,7 @@ int convrot_tree_masks(const int32_t* parents, const int32_t* cu, const int32_t*
   if (parents == nullptr || cu == nullptr || lens == nullptr || mask == nullptr || pos == nullptr) return CONVROT_ERR_NULL;
   if (!aligned(parents, 4) || !aligned(cu, 4) || !aligned(lens, 4) || !aligned(mask, 8) || !aligned(pos, 8))
     return CONVROT_ERR_ALIGN;
-  for (const auto& [out, bytes] : {std::pair<const void*, int64_t>{mask, 8 * T * words}, {pos, 8 * T}})
+  for (const auto& [out, bytes] : {Extent{mask, 8 * T * words}, {pos, 8 * T}})
     if (!apart(out, bytes, parents, 4 * T) || !apart(out, bytes, cu, 4 * (B + 1)) || !apart(out, bytes, lens, 4 * B))
       return CONVROT_ERR_SHAPE;
   if (!apart(mask, 8 * T * words, pos, 8 * T)) return CONVROT_ERR_SHAPE;
@@ -169,8 +165,7 @@ int convrot_lora(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t l
   if (!apart(out, bytes_of(M, N, ldo, 2), x, bytes_of(M, K, ldx, size))) return CONVROT_ERR_SHAPE;
   const int64_t need = int64_t(convrot_lora_workspace_bytes(M, K, r, L));
   if (ws_bytes < size_t(need)) return CONVROT_ERR_WORKSPACE;
-  for (const auto& [other, bytes] : {std::pair<const void*, int64_t>{ids, 4 * M}, {a, 2 * L * r * K}, {b, 2 * L * N * r},
-                                     {scale, 4 * L}, {workspace, need}})
+  for (const auto& [other, bytes] : {Extent{ids, 4 * M}, {a, 2 * L * r * K}, {b, 2 * L * N * r}, {scale, 4 * L}, {workspace, need}})
     if (!apart(out, bytes_of(M, N, ldo, 2), other, bytes)) return CONVROT_ERR_SHAPE;
   convrot::LoraArgs args{};
   args.x = x;

@@ -240,3 +240,25 @@ def test_lora_answers_over_other_tensors(lib):
     for name, n in size.items():
         for out in (at[name], at[name] + n - 2, at[name] - mine + 2):
             assert call(out) == call(out, out) == E.CONVROT_ERR_SHAPE, name
+
+
+def test_turned_heads_over_positions_frequencies_and_weights(lib):
+    """An output lies over no tensor of the call, the small ones included."""
+    T, H, D, R, far = 3, 4, 64, 32, 0x100000
+    mine = 2 * T * H * D
+
+    def call(fn, **k):
+        qo, ko = k.get("qo", far * 10), k.get("ko", far * 11)
+        args = [far * 8, H * D, D, qo, H * D, D, H, far * 9, H * D, D, ko, H * D, D, H, 1, T, D, R, k.get("pos", far), k.get("inv", far * 2)]
+        if fn is lib.convrot_norm_rotary:
+            args += [k.get("qw", far * 3), k.get("kw", far * 4), 0, ctypes.c_float(1e-6), 0, ctypes.c_float(1.0), None]
+        else:
+            args += [0, ctypes.c_float(1.0), 0, None]
+        return fn(*args)
+    size = {"pos": (1, 8 * T), "inv": (2, 2 * R), "qw": (3, 4 * D), "kw": (4, 4 * D)}
+    for fn, names in ((lib.convrot_rotary, ("pos", "inv")), (lib.convrot_norm_rotary, ("pos", "inv", "qw", "kw"))):
+        for name in names:
+            n, bytes_ = size[name]
+            for out in (far * n, far * n + bytes_ - 2, far * n - mine + 2):
+                assert call(fn, qo=out) == call(fn, ko=out) == E.CONVROT_ERR_SHAPE, name
+    assert call(lib.convrot_norm_rotary, qw=far * 3 + 2) == E.CONVROT_ERR_ALIGN
