@@ -4,7 +4,7 @@
 
 namespace {
 
-constexpr int64_t kMaxWords = 1024, kMaxAdapters = 1 << 24;
+constexpr int64_t kMaxWords = 1024, kMaxAdapters = 1 << 24, kMaxPageBytes = 1 << 29;
 constexpr float kLeastEps = 7.888609052210118e-31f;     // 2^-100
 
 int check_lora(int64_t M, int64_t K, int64_t r, int64_t L) {
@@ -125,7 +125,7 @@ int convrot_kv8_copy(const int32_t* src, const int32_t* dst, int64_t n, int8_t* 
   if (st != CONVROT_OK) return st;
   if (n < 0 || n > kIntMax) return CONVROT_ERR_SHAPE;
   const convrot::Kv8Cache cache{kc, ks, vc, vs, num_pages, int(page), int(H), int(D)};
-  if (!launch_fits(n, 256) || convrot::kv8_copy_parts(cache) > 65535) return CONVROT_ERR_UNSUPPORTED;
+  if (!launch_fits(n, 256) || H * page * D > kMaxPageBytes) return CONVROT_ERR_UNSUPPORTED;
   if (n == 0) return CONVROT_OK;
   if (src == nullptr || dst == nullptr || kc == nullptr || ks == nullptr || vc == nullptr || vs == nullptr)
     return CONVROT_ERR_NULL;

@@ -155,11 +155,10 @@ hipError_t launch_kv8_tree_attention(const void* q, int dtype, int64_t q_t, int6
                                      float scale, const Kv8Plan& p, uint16_t* out, void* workspace,
                                      hipStream_t stream);
 
-// Tokens and pages moved within the cache (kv8_pages.hip); a copy takes n * kv8_copy_parts workgroups.
+// Tokens and pages moved within the cache (kv8_pages.hip).
 size_t kv8_keep_bytes(int64_t T, int64_t B, int64_t H, int64_t D);
 hipError_t launch_kv8_keep(const int32_t* kept, const Kv8Batch& b, const Kv8Cache& c, int64_t max_new, int32_t* lens_out,
                            void* workspace, hipStream_t stream);
-int64_t kv8_copy_parts(const Kv8Cache& c);
 hipError_t launch_kv8_copy(const int32_t* src, const int32_t* dst, int64_t n, const Kv8Cache& c, hipStream_t stream);
 
 // Low-rank adapters (lora.hip): out = y + scale[id] (x A[id]^T) B[id]^T.

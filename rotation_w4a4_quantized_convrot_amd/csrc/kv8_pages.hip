@@ -340,12 +340,12 @@ constexpr int kCopyBytes = kThreads * 16 * 4;     // of a workgroup
 // of 64 tokens, 8 heads of 128 (655 MB): 127 to 137 us, 5.0 TB/s, as a large copy; 13 small pages 3.5 us, the launch.
 __global__ __launch_bounds__(kThreads) void copy_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
                                                         Kv8Cache cache) {
-  const bool values = blockIdx.y & 1;
+  const bool values = blockIdx.z;
   const int64_t from = src[blockIdx.x], to = dst[blockIdx.x];
   if (from < 0 || from >= cache.num_pages || to < 0 || to >= cache.num_pages || from == to) return;
   const int64_t bytes = int64_t(cache.H) * cache.page * cache.D;
   int8_t* const codes = values ? cache.vc : cache.kc;
-  const int64_t part = int64_t(blockIdx.y >> 1) * kCopyBytes;
+  const int64_t part = int64_t(blockIdx.y) * kCopyBytes;
   const uint4_t* const in = reinterpret_cast<const uint4_t*>(codes + from * bytes + part);
   uint4_t* const out = reinterpret_cast<uint4_t*>(codes + to * bytes + part);
   const int64_t left = (bytes - part) / 16;
@@ -356,7 +356,7 @@ __global__ __launch_bounds__(kThreads) void copy_kernel(const int32_t* __restric
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (threadIdx.x + i * kThreads < left) out[threadIdx.x + i * kThreads] = w[i];
-  if (blockIdx.y < 2) {
+  if (blockIdx.y == 0) {
     float* const scales = values ? cache.vs : cache.ks;
     for (int h = threadIdx.x; h < cache.H; h += kThreads) scales[to * cache.H + h] = scales[from * cache.H + h];
   }
@@ -412,11 +412,9 @@ hipError_t launch_kv8_keep(const int32_t* kept, const Kv8Batch& b, const Kv8Cach
   return launch_kernel(put, dim3(unsigned(2 * b.B * c.H), unsigned(pages + 1)), dim3(kThreads), 0, stream, b, c, s);
 }
 
-int64_t kv8_copy_parts(const Kv8Cache& c) { return 2 * ceil_div(int64_t(c.H) * c.page * c.D, kCopyBytes); }
-
 hipError_t launch_kv8_copy(const int32_t* src, const int32_t* dst, int64_t n, const Kv8Cache& c, hipStream_t stream) {
-  return launch_kernel(copy_kernel, dim3(unsigned(n), unsigned(kv8_copy_parts(c))), dim3(kThreads), 0, stream, src, dst,
-                       c);
+  const int64_t parts = ceil_div(int64_t(c.H) * c.page * c.D, kCopyBytes);      // 2^15 for the largest page
+  return launch_kernel(copy_kernel, dim3(unsigned(n), unsigned(parts), 2), dim3(kThreads), 0, stream, src, dst, c);
 }
 
 }  // namespace convrot

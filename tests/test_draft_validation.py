@@ -262,3 +262,9 @@ def test_turned_heads_over_positions_frequencies_and_weights(lib):
             for out in (far * n, far * n + bytes_ - 2, far * n - mine + 2):
                 assert call(fn, qo=out) == call(fn, ko=out) == E.CONVROT_ERR_SHAPE, name
     assert call(lib.convrot_norm_rotary, qw=far * 3 + 2) == E.CONVROT_ERR_ALIGN
+
+
+def test_copy_of_the_largest_pages(lib):
+    """H page D up to 2^29, on either side of it."""
+    call = lambda H: lib.convrot_kv8_copy(None, A, 3, A, A, A, A, 10, 128, H, 256, None)  # noqa: E731
+    assert call(2 ** 14) == E.CONVROT_ERR_NULL and call(2 ** 14 + 1) == E.CONVROT_ERR_UNSUPPORTED

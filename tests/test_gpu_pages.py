@@ -229,3 +229,19 @@ def test_graph_and_stream(cr, pad):
         want = run(other)
         torch.cuda.synchronize()
         assert torch.equal(after, want) and all(torch.equal(a, b) for a, b in zip(cache, other))
+
+
+def test_copy_of_the_largest_page(cr):
+    """H page D = 2^29: its last codes and scales move too."""
+    print("\n[case] copy, the largest page", flush=True)
+    H, page, D = 1 << 14, 128, 256
+    kc, vc = (torch.zeros((3, H, *s), dtype=torch.int8, device=DEV) for s in ((page, D), (D, page)))
+    ks, vs = (torch.rand((3, H), device=DEV) for _ in range(2))
+    for t in (kc, vc):
+        t[2].copy_(torch.randint(-127, 128, t.shape[2:], device=DEV, dtype=torch.int8))
+        t[2, -1, -1, -1], t[2, 0, 0, 0] = 77, 55
+        t[2, H // 2:] += 1
+    cr.convrot_kv8_copy(i32([2]).to(DEV), i32([0]).to(DEV), kc, ks, vc, vs)
+    for t in (kc, ks, vc, vs):
+        assert torch.equal(t[0], t[2])
+    assert not bool(kc[1].any()) and not bool(vc[1].any())
