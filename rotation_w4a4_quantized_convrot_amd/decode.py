@@ -664,6 +664,7 @@ class LowRankAdapters(torch.nn.Module):
         self.register_buffer("b", torch.zeros((count, out_features, rank), dtype=torch.bfloat16, device=device))
         self.register_buffer("scale", torch.zeros((count,), dtype=torch.float32, device=device))
 
+    @torch.no_grad()
     def set_adapter(self, index: int, a: torch.Tensor, b: torch.Tensor, scale: float = 1.0) -> None:
         """a [r, in_features], b [out_features, r], r up to the rank: the rest of the ranks are zeros."""
         r = a.shape[0]

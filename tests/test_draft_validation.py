@@ -268,3 +268,14 @@ def test_copy_of_the_largest_pages(lib):
     """H page D up to 2^29, on either side of it."""
     call = lambda H: lib.convrot_kv8_copy(None, A, 3, A, A, A, A, 10, 128, H, 256, None)  # noqa: E731
     assert call(2 ** 14) == E.CONVROT_ERR_NULL and call(2 ** 14 + 1) == E.CONVROT_ERR_UNSUPPORTED
+
+
+def test_adapters_set_from_parameters():
+    """Trained pairs are parameters: the module keeps their values, not their history."""
+    import copy
+    m = cr.LowRankAdapters(2, 8, 64, 32)
+    a, b = torch.nn.Parameter(torch.ones(3, 64)), torch.nn.Parameter(torch.ones(32, 3))
+    scale = torch.nn.Parameter(torch.tensor(0.5))
+    m.set_adapter(1, a, b, scale)
+    assert not any(t.requires_grad for t in (m.a, m.b, m.scale)) and m.a[1].float().sum() == 3 * 64 and m.scale[1] == 0.5
+    copy.deepcopy(m)
