@@ -679,6 +679,8 @@ class LowRankAdapters(torch.nn.Module):
 
     def forward(self, x: torch.Tensor, y: torch.Tensor, ids: torch.Tensor) -> torch.Tensor:
         """Adds to y [M, out_features], in place, what the rows' adapters make of x [M, in_features]."""
+        if x.dim() == 2 and not x.is_contiguous() and (x.stride(1) != 1 or x.stride(0) < x.shape[1]):
+            x = x.contiguous()                             # as the projection takes it; strided rows go as they are
         return convrot_lora(x, ids, self.a, self.b, self.scale, y, out=y)
 
 

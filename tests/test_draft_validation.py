@@ -279,3 +279,13 @@ def test_adapters_set_from_parameters():
     m.set_adapter(1, a, b, scale)
     assert not any(t.requires_grad for t in (m.a, m.b, m.scale)) and m.a[1].float().sum() == 3 * 64 and m.scale[1] == 0.5
     copy.deepcopy(m)
+
+
+def test_adapters_take_rows_as_the_projection_does():
+    """Columns apart, rows broadcast, rows that overlap: the linear layer beside the adapters takes them."""
+    m = cr.LowRankAdapters(2, 8, 64, 32)
+    y, ids = z((5, 32)), z(5, i32)
+    for x in (z((64, 5)).t(), z((5, 128))[:, ::2], z((1, 64)).expand(5, 64), z(80).as_strided((5, 64), (4, 1))):
+        _reaches_device(m, x, y, ids)
+    _raises(m, z((5, 63)), y, ids)
+    _raises(m, z(64), y, ids)

@@ -245,3 +245,20 @@ def test_infinite_weights(cr, M, K, N, r, dtype):
         size = O.lora(x, ids, a.nan_to_num(0, 0, 0), b.nan_to_num(0, 0, 0), scale, y)[1]
         tol = size * (2 * 2.0 ** -16 + (K + 2 * r + 64) * 2.0 ** -24 + 2.0 ** -23) + 2.0 ** -8 * ref.abs()
         assert bool(((out - ref).abs() <= tol)[good].all())
+
+
+def test_module_with_rows_of_any_strides(cr):
+    """What the linear layer beside the adapters takes: columns apart, rows broadcast, rows that overlap."""
+    print("\n[case] lora module, strides of x", flush=True)
+    gen = torch.Generator().manual_seed(12)
+    K, N = 64, 40
+    for M in (6, 80):
+        m = cr.LowRankAdapters(2, 8, K, N, device=DEV)
+        args = inputs(M, K, N, 8, 2, torch.bfloat16, M)
+        m.a.copy_(args[2]), m.b.copy_(args[3]), m.scale.copy_(args[4])
+        store = torch.randn((M, 2 * K), generator=gen).to(torch.bfloat16)
+        for view in (lambda s: s[:, ::2], lambda s: s[:, :K], lambda s: s[:1, :K].expand(M, K),
+                     lambda s: s.flatten()[:M * K].view(K, M).t(), lambda s: s.as_strided((M, K), (K // 2, 1))):
+            y = args[5].to(DEV)
+            m(view(store.to(DEV)), y, args[1].to(DEV))
+            check(y, view(store), *args[1:])
