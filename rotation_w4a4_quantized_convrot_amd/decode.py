@@ -269,7 +269,8 @@ def convrot_norm_rotary(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.T
     q_weight and k_weight [D] (bf16/fp32, both of one dtype; None: ones) -> (q_out, k_out)."""
     if k is None and k_weight is not None:
         raise ValueError("k_weight without k")
-    _is_tensor(q, "q")
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        _heads(q, "q")                      # says what is wrong
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
             _is_tensor(w, name)

@@ -289,3 +289,12 @@ def test_adapters_take_rows_as_the_projection_does():
         _reaches_device(m, x, y, ids)
     _raises(m, z((5, 63)), y, ids)
     _raises(m, z(64), y, ids)
+
+
+def test_normed_heads_name_what_is_wrong():
+    """A query tensor that is none is reported as such, not as a weight of the wrong size."""
+    pos, inv = z(3, i64), z(16, f32)
+    for q in (z((3, 64)), z(64), z((3, 4, 64, 1))):
+        _raises(cr.convrot_norm_rotary, q, None, pos, inv, z(64), match="q must be 3-D")
+        _raises(cr.convrot_norm_rotary, z((3, 4, 64)), q, pos, inv, z(64), z(64), match="k must be 3-D")
+    _raises(cr.convrot_norm_rotary, z((3, 4, 64), torch.float16), None, pos, inv, z(64), exc=TypeError)
