@@ -137,6 +137,7 @@ struct Kv8Plan {
   int row_tiles;       // 16-row tiles of a workgroup: 1, 2 or 4 (few rows), 8 or 16 (many)
   int64_t row_blocks;  // per sequence and cached head
   int splits;          // of a sequence's tokens
+  int64_t sums;        // rows of partial sums in the workspace, before what the splits' join needs to know of them
   size_t bytes;
   int64_t threads;     // of its largest launch
 };

@@ -307,8 +307,8 @@ Kv8Plan plan_kv8_attention(int64_t B, int64_t T, int64_t Hq, int64_t H, int64_t 
   const int64_t hold = many || D > 128 ? 256 : 512;
   const int64_t wish = many ? hold / groups : ceil_div(hold, groups);
   p.splits = int(std::min<int64_t>(std::max<int64_t>(1, wish), std::min<int64_t>(std::max<int64_t>(1, blocks / 8), 256)));
-  if (p.splits > 1)
-    p.bytes = round256(size_t(p.splits) * T * Hq * D * 4) + round256(size_t(p.splits) * T * Hq * 8);
+  p.sums = p.splits * T * Hq;
+  if (p.splits > 1) p.bytes = round256(size_t(p.sums) * D * 4) + round256(size_t(p.sums) * 8);
   // joining the splits takes up to a workgroup a row
   p.threads = std::max(groups * p.splits * (many ? 512 : 256), p.splits > 1 ? T * Hq * 256 : 0);
   return p;

@@ -95,9 +95,14 @@ struct AttentionArgs {
   float scale;
   int64_t row_blocks, rows;       // rows: T * Hq, of the partial results
   uint16_t* out;
-  float* partial;                 // [splits][rows][D], or NULL: one split, straight to out
+  float* partial;                 // [splits][rows][D] (but for TreeTokens::whole), or NULL: one split, straight to out
   float2* stats;                  // [splits][rows]: reference and sum
 };
+
+// [splits][rows], behind the statistics: where partial has a piece's row, for TreeTokens::whole.
+__host__ __device__ __forceinline__ uint32_t* places_of(const AttentionArgs& a) {
+  return reinterpret_cast<uint32_t*>(a.stats + a.splits * a.rows);
+}
 
 // What a workgroup works on: a block of the rows of one sequence and cached head, and a share of
 // the sequence's tokens in blocks of 64.
@@ -225,7 +230,10 @@ struct EarlierTokens {};
 struct TreeTokens {
   const uint64_t* mask;         // [T][words]
   int64_t words;
-  bool whole;                   // many rows: what one workgroup has seen all of goes straight to out
+  // many rows: what one workgroup has seen all of goes straight to out; partial has two slots of rows for every
+  // workgroup, for the group that it begins within and the one that it begins but does not end, and places_of says
+  // where it has a row of a piece
+  bool whole;
 };
 
 // A lane's row.  hide: scores of the lane's 16 tokens from `token` on become -infinity where they are not seen
@@ -416,9 +424,9 @@ __device__ __forceinline__ uint2_t pack_bf16x4(const float4_t& v, float mul) {
 }
 
 // Four values of a row's answer, or of its share of the sums.
-__device__ __forceinline__ void put(const AttentionArgs& a, float* partial, int D, int64_t split, int64_t row, int d,
+__device__ __forceinline__ void put(const AttentionArgs& a, float* partial, int D, int64_t place, int64_t row, int d,
                                     const float4_t& v, float over_l) {
-  if (partial != nullptr) *reinterpret_cast<float4_t*>(partial + (split * a.rows + row) * D + d) = v;
+  if (partial != nullptr) *reinterpret_cast<float4_t*>(partial + place * D + d) = v;
   else *reinterpret_cast<uint2_t*>(a.out + row * D + d) = pack_bf16x4(v, over_l);
 }
 
@@ -635,7 +643,7 @@ __global__ __launch_bounds__(256, DT <= 128 ? 2 : 1) void few_rows_kernel(Attent
 #pragma unroll
         for (int p = 1; p < kPhases; ++p)
           v += *reinterpret_cast<const float4_t*>(&sums[((t + p * TILES) * 16 + i) * kOStride + d]);
-        put(a, a.partial, cache.D, w.split, row, d, v, over_l);
+        put(a, a.partial, cache.D, w.split * a.rows + row, row, d, v, over_l);
       }
     }
   }
@@ -887,12 +895,20 @@ __device__ __forceinline__ void many_rows(const AttentionArgs& a, const Kv8Batch
     const int64_t r = r0 + rt * 16 + n;
     if (r >= w.rows) continue;
     const int64_t row = (w.seq.row0 + uint32_t(r) / uint32_t(G)) * a.Hq + w.h * G + uint32_t(r) % uint32_t(G);
-    if (a.partial != nullptr && c == 0) a.stats[max(w.split, int64_t(0)) * a.rows + row] = make_float2(m[rt], w.split < 0 ? -1.0f : l[rt]);
+    const int64_t at = max(w.split, int64_t(0)) * a.rows + row;
+    int64_t place = at;
+    if constexpr (std::is_same_v<Seen, TreeTokens>)
+      if (seen.whole) place = (2 * int64_t(blockIdx.x) + (from == 0)) * kRows + (r - rb * kRows);
+    if (a.partial != nullptr && c == 0) {
+      a.stats[at] = make_float2(m[rt], w.split < 0 ? -1.0f : l[rt]);
+      if constexpr (std::is_same_v<Seen, TreeTokens>)
+        if (seen.whole) places_of(a)[at] = uint32_t(place);
+    }
     const float over_l = l[rt] == 0.0f ? 0.0f : 1.0f / l[rt];
 #pragma unroll
     for (int dt = 0; dt < kTilesD; ++dt) {
       const int d = 16 * dt + 4 * c;
-      if (d < cache.D) put(a, w.split < 0 ? nullptr : a.partial, cache.D, w.split, row, d, o[dt][rt], over_l);
+      if (d < cache.D) put(a, w.split < 0 ? nullptr : a.partial, cache.D, place, row, d, o[dt][rt], over_l);
     }
   }
 }
@@ -988,7 +1004,8 @@ hipError_t run_kernel(Kernel* kernel, int64_t groups, int threads, size_t lds, c
 template <typename TIn, int DT>
 hipError_t run_tree(const AttentionArgs& a, const Kv8Batch& b, const Kv8Cache& c, const TreeTokens& tree,
                     const Kv8Plan& p, hipStream_t stream);
-hipError_t join_pieces(const AttentionArgs& a, const Kv8Batch& b, const Kv8Cache& c, const Kv8Plan& p, hipStream_t stream);
+hipError_t join_pieces(const AttentionArgs& a, const Kv8Batch& b, const Kv8Cache& c, const TreeTokens& tree,
+                       const Kv8Plan& p, hipStream_t stream);
 
 template <typename TIn, int DT, typename Seen>
 hipError_t run_attention(const AttentionArgs& a, const Kv8Batch& b, const Kv8Cache& c, const Seen& seen,
@@ -1032,14 +1049,13 @@ hipError_t attend(const void* q, int dtype, int64_t q_t, int64_t q_h, int64_t Hq
   a.out = out;
   if (p.splits > 1) {
     a.partial = static_cast<float*>(workspace);
-    a.stats = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) +
-                                        round256(size_t(p.splits) * a.rows * c.D * 4));
+    a.stats = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + round256(size_t(p.sums) * c.D * 4));
   }
   const hipError_t e = dtype == 0 ? run_attention<float>(a, b, c, seen, p, stream)
                                   : run_attention<uint16_t>(a, b, c, seen, p, stream);
   if (e != hipSuccess || p.splits == 1) return e;
   if constexpr (std::is_same_v<Seen, TreeTokens>)
-    if (p.row_tiles > 4) return join_pieces(a, b, c, p, stream);
+    if (p.row_tiles > 4) return join_pieces(a, b, c, seen, p, stream);
   // a wave to a row; four where there are many splits
   if (p.splits <= 8)
     return launch_kernel(join_splits_kernel<1>, dim3(unsigned(ceil_div(a.rows, 4))), dim3(256), 0, stream, b,

@@ -55,7 +55,10 @@ __global__ __launch_bounds__(kThreads) void tree_masks_kernel(const int32_t* __r
 // what it costs to begin with it and one for each block, and a workgroup takes the next `share` units; where
 // that ends within a group the next one goes on there, unless it would leave fewer than kLeast blocks on one side.
 // A group that is not cut may be written as it is, with a mark for the join (writes_whole); else every piece leaves its sums in the
-// workspace, and the last one of a group says so for the pieces that it does not have.  The lengths are the device's, so each workgroup finds its part by going over the batch.
+// workspace, and the last one of a group says so for the pieces that it does not have.  Where groups that are not cut are
+// written, a workgroup has two slots for the sums of the others: 512 slots of 256 rows, 64 MB for heads of 128, whatever
+// the number of rows (with sums for every row and piece, 100 trees of 64 with 32 heads of 128 took 420 MB).  The lengths
+// are the device's, so each workgroup finds its part by going over the batch.
 //
 // Trees of 300 and 159 tokens over 20000 and 8545, 64 / 8 heads of 128: 340 us (720 TFLOP/s;
 // with splits of the longest context, as for rows that see the tokens up to their own, about 630); 16 trees of up to 26 over up
@@ -218,7 +221,8 @@ bool writes_whole(int64_t rows, int D) { return rows * join_lanes(D) > int64_t(4
 template <int LANES, bool WHOLE>
 __global__ __launch_bounds__(256) void join_pieces_kernel(Kv8Batch batch, int Hq, int D, int splits, int64_t rows,
                                                           const float* __restrict__ partial,
-                                                          const float2* __restrict__ stats, uint16_t* __restrict__ out) {
+                                                          const float2* __restrict__ stats,
+                                                          const uint32_t* __restrict__ places, uint16_t* __restrict__ out) {
   constexpr int kBatch = 8;
   const int lane = threadIdx.x & 63, n = lane & (LANES - 1);
   const int64_t row = (int64_t(blockIdx.x) * 256 + threadIdx.x) / LANES;
@@ -233,9 +237,14 @@ __global__ __launch_bounds__(256) void join_pieces_kernel(Kv8Batch batch, int Hq
   constexpr uint64_t kMask = LANES == 64 ? ~uint64_t(0) : (uint64_t(1) << (LANES & 63)) - 1;
   const bool some = (__ballot(there) >> (lane & ~(LANES - 1)) & kMask) != 0;
   float2 st[kBatch];
+  uint32_t place[WHOLE ? kBatch : 1];     // of the piece's row in partial
   const auto load = [&](int from) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) st[i] = stats[int64_t(min(from + i, splits - 1)) * rows + at];
+    for (int i = 0; i < kBatch; ++i) {
+      const int64_t piece = int64_t(min(from + i, splits - 1)) * rows + at;
+      st[i] = stats[piece];
+      if constexpr (WHOLE) place[i] = places[piece];
+    }
   };
   float top = kNothing;
   bool open = true;
@@ -253,8 +262,12 @@ __global__ __launch_bounds__(256) void join_pieces_kernel(Kv8Batch batch, int Hq
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       p[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-      if (open && from + i < splits && st[i].y != 0.0f && n * 4 < D)      // nothing seen there, nothing written
-        p[i] = *reinterpret_cast<const float4_t*>(partial + ((from + i) * rows + at) * D + n * 4);
+      // nothing seen there, nothing written; and places of rows of no sequence are not to be followed
+      if ((!WHOLE || some) && open && from + i < splits && st[i].y != 0.0f && n * 4 < D) {
+        int64_t from_row = (from + i) * rows + at;
+        if constexpr (WHOLE) from_row = place[i];
+        p[i] = *reinterpret_cast<const float4_t*>(partial + from_row * D + n * 4);
+      }
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -279,14 +292,15 @@ hipError_t run_tree(const AttentionArgs& a, const Kv8Batch& b, const Kv8Cache& c
   else return hipErrorInvalidValue;                    // no plan has such tiles
 }
 
-hipError_t join_pieces(const AttentionArgs& a, const Kv8Batch& b, const Kv8Cache& c, const Kv8Plan& p, hipStream_t stream) {
+hipError_t join_pieces(const AttentionArgs& a, const Kv8Batch& b, const Kv8Cache& c, const TreeTokens& tree,
+                       const Kv8Plan& p, hipStream_t stream) {
   const int lanes = join_lanes(c.D);
-  const bool whole = writes_whole(a.rows, c.D);
+  const bool whole = tree.whole;
   auto kernel = lanes == 16 ? (whole ? join_pieces_kernel<16, true> : join_pieces_kernel<16, false>)
                 : lanes == 32 ? (whole ? join_pieces_kernel<32, true> : join_pieces_kernel<32, false>)
                               : (whole ? join_pieces_kernel<64, true> : join_pieces_kernel<64, false>);
   return launch_kernel(kernel, dim3(unsigned(ceil_div(a.rows, 256 / lanes))), dim3(256), 0, stream, b, a.Hq, c.D, p.splits,
-                       a.rows, a.partial, a.stats, a.out);
+                       a.rows, a.partial, a.stats, places_of(a), a.out);
 }
 
 }  // namespace
@@ -317,7 +331,10 @@ Kv8Plan plan_kv8_tree(int64_t B, int64_t T, int64_t Hq, int64_t H, int64_t D, in
   // pieces: twice what equal sequences have of equal parts for every workgroup, for ragged ones
   const int64_t groups = B * H * p.row_blocks;
   p.splits = int(2 + 2 * std::min<int64_t>(ceil_div(kParts, groups), ceil_div(blocks, kShare)));
-  p.bytes = round256(size_t(p.splits) * T * Hq * D * 4) + round256(size_t(p.splits) * T * Hq * 8);
+  const size_t all = size_t(p.splits) * T * Hq;
+  const bool whole = writes_whole(T * Hq, int(D));
+  p.sums = whole ? 2 * kParts * 16 * p.row_tiles : int64_t(all);
+  p.bytes = round256(size_t(p.sums) * D * 4) + round256(all * (whole ? 12 : 8));
   const int lanes = join_lanes(int(D));
   p.threads = std::max<int64_t>(kParts * 512, ceil_div(T * Hq, 256 / lanes) * 256);
   return p;

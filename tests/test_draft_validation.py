@@ -298,3 +298,13 @@ def test_normed_heads_name_what_is_wrong():
         _raises(cr.convrot_norm_rotary, q, None, pos, inv, z(64), match="q must be 3-D")
         _raises(cr.convrot_norm_rotary, z((3, 4, 64)), q, pos, inv, z(64), z(64), match="k must be 3-D")
     _raises(cr.convrot_norm_rotary, z((3, 4, 64), torch.float16), None, pos, inv, z(64), exc=TypeError)
+
+
+def test_tree_attention_workspace_does_not_grow_with_the_answer(lib):
+    """Only groups that are cut between workgroups leave sums: 512 of up to 256 rows, and what says where they are."""
+    size = cr.convrot_kv8_tree_attention_workspace_bytes
+    for T, B, Hq, H, D, new, length in ((27000, 270, 64, 8, 128, 100, 9000), (6400, 100, 32, 8, 128, 64, 600), (30000, 300, 64, 8, 128, 30000, 8192),
+                                        (2 ** 21 - 1, 5, 64, 8, 128, 9, 100), (2 ** 20 - 1, 5, 64, 8, 256, 9, 100),
+                                        (1000000, 100, 8, 1, 64, 10000, 100), (40000, 1, 16, 2, 192, 40000, 100000)):
+        need = size(T, B, Hq, H, D, new, length)
+        assert 0 < need <= 512 * 256 * D * 4 + 16 * 12 * T * Hq + 4096, (T, B, Hq, H, D, need)

@@ -466,3 +466,39 @@ def test_many_trees_with_default_hints(cr):
     for b in (0, 1, 150, 298, 299):
         at = slice(b * n, b * n + n)
         check(out[at], q[at], mask[at], cum([n]), ln[b:b + 1], table[b:b + 1], cache, 16, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("B,Hq,H,D", [(30, 40, 2, 64), (9, 64, 8, 128), (12, 16, 2, 256), (20, 30, 1, 80)])
+def test_cut_groups_leave_their_sums_in_slots(cr, B, Hq, H, D):
+    """So many rows that whole groups are written, over contexts so long and ragged that many groups are cut, some into
+    several pieces; rows of no sequence before, behind and between the others; a workspace of the stated size whose
+    other bytes hold NaN, a second time with zeros."""
+    print(f"\n[case] tree attention, cut groups of {B} trees, H={Hq}/{H} D={D}", flush=True)
+    gen = torch.Generator().manual_seed(B + D)
+    page = 64
+    new = [int(torch.randint(30, 120, (1,), generator=gen)) for _ in range(B)]
+    lens = [n + int(torch.randint(0, 200, (1,), generator=gen)) for n in new]
+    lens[1], lens[B // 2], lens[-1] = new[1] + 9000, new[B // 2] + 3000, new[-1] + 700
+    table, pages = paging(lens, page, gen)
+    cache = cache_of(pages, H, page, D, gen)
+    T = sum(new) + 500 + max(0, (1 << 20) // (16 if D <= 64 else 32 if D <= 128 else 64) // Hq)
+    cu, ln = cum(new) + 7, i32(lens)
+    q = torch.randn((T, Hq, D), generator=gen).to(torch.bfloat16)
+    mask = random_mask(T, 2, gen)
+    args = (q.to(DEV), mask.to(DEV), cu.to(DEV), ln.to(DEV), table.to(DEV), *to(cache))
+    hints = {"max_new": max(new), "max_len": max(lens)}
+    need = cr.convrot_kv8_tree_attention_workspace_bytes(T, B, Hq, H, D, *hints.values())
+    outs = []
+    for fill in (0xFF, 0):
+        store = torch.full((need + 512,), fill, dtype=torch.uint8, device=DEV)
+        out = torch.full((T, Hq, D), 3.0, dtype=torch.bfloat16, device=DEV)
+        cr.convrot_kv8_tree_attention(*args, g=16, out=out, workspace=store[:need], **hints)
+        assert bool((store[need:] == fill).all())
+        outs.append(out)
+    assert torch.equal(*outs)
+    assert bool((outs[0][:7] == 3).all()) and bool((outs[0][7 + sum(new):] == 3).all())
+    for b in (0, 1, 2, B // 2, B - 1):
+        at = slice(int(cu[b]), int(cu[b + 1]))
+        heads = slice(0, Hq // H)                              # of the first cached head
+        one = (cache[0][:, :1], cache[1][:, :1], cache[2][:, :1], cache[3][:, :1])
+        check(outs[0][at, heads], q[at, heads], mask[at], cum([new[b]]), ln[b:b + 1], table[b:b + 1], one, 16, 1 / math.sqrt(D))
