@@ -507,7 +507,8 @@ CONVROT_API int convrot_norm_rotary(const void* q, int64_t q_t, int64_t q_h, voi
  *     descends from it; rows from 64 words on have no bits;
  *   pos int64 [T]: lens[b] - n + the number of the row's ancestors: its rotary position.
  * words 1 to 1024; mask and pos 8-byte aligned, over no other tensor of the call.  max_new sizes the launch only.  Rows of no sequence are left as they
- * were.  T = 0 or B = 0 is a no-op.  Errors: SHAPE, UNSUPPORTED, NULL, ALIGN, HIP. */
+ * were.  A row takes time by the number of its ancestors.  T = 0 or B = 0 is a no-op.
+ * Errors: SHAPE, UNSUPPORTED, NULL, ALIGN, HIP. */
 CONVROT_API int convrot_tree_masks(const int32_t* parents, const int32_t* cu, const int32_t* lens, int64_t B, int64_t T,
                                    int64_t max_new, int64_t words, uint64_t* mask, int64_t* pos, void* stream);
 
@@ -567,8 +568,9 @@ CONVROT_API int convrot_kv8_copy(const int32_t* src, const int32_t* dst, int64_t
  * out is y (the same pointer and row stride), and else apart from every tensor of the call and from the workspace: from its
  * first element to its last it reaches into none of theirs (SHAPE), also where views of one buffer lie between one
  * another.  M = 0 or N = 0 is a no-op.
- * 1 <= L <= 2^24, 1 <= r <= 256, M <= 4194240.  workspace 256-byte aligned.  Results do not depend on the run; rows do not
- * depend on one another.  Errors: DTYPE, SHAPE, UNSUPPORTED, NULL, ALIGN, WORKSPACE, HIP. */
+ * 1 <= L <= 2^24, 1 <= r <= 256, M <= 4194240.  workspace 256-byte aligned.  Results do not depend on the run, nor a
+ * row's on what the other rows hold or where they stand; in a call of another M a row may differ in its last bits, since M
+ * decides how the sums are split.  Errors: DTYPE, SHAPE, UNSUPPORTED, NULL, ALIGN, WORKSPACE, HIP. */
 CONVROT_API size_t convrot_lora_workspace_bytes(int64_t M, int64_t K, int64_t r, int64_t L);
 CONVROT_API int convrot_lora(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx, const int32_t* ids,
                              const void* a, const void* b, const float* scale, int64_t r, int64_t L, const void* y,

@@ -5,7 +5,7 @@
 // h first, in fp32, split over K into partial sums that the second launch adds up in their order.  Both
 // products run on v_mfma_f32_16x16x32_bf16; A and B are bf16 already, fp32 operands (x where it is fp32, and h)
 // enter as two bf16 pieces, the value cut off and its rest: 2^-16 relative, below 2^-133 an absolute 2^-134.  A
-// row's sums do not depend on the rows beside it, nor on its place in a tile.
+// row's sums do not depend on what the rows beside it hold, nor on its place in a tile; how they are split goes by M.
 //
 // Few rows: a workgroup to each row of a tile of 16, of which the first with its adapter goes on, for all rows
 // of the tile that have it; operands go straight into registers.  Many rows: the rows are sorted by adapter
@@ -638,7 +638,8 @@ __global__ __launch_bounds__(kWaves * 64) void many_expand_kernel(LoraArgs a, in
 }
 
 // Both ways, whole calls of 8192 -> 8192, r = 32: 100 rows of one adapter 26 us as few, 18 as many rows, of 64 adapters 26
-// and 39; 256 rows 34 and 19, 42 and 40; 64 rows of one or 64 adapters 18 and 21 as few.
+// and 39; 256 rows 34 and 19, 42 and 40; 64 rows of one or 64 adapters 18 and 21 as few.  How many adapters the rows use is
+// known to the device only; the rule takes them for few.
 constexpr int64_t kFewRows = 64;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
