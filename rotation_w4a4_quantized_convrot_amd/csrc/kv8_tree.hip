@@ -56,7 +56,7 @@ __global__ __launch_bounds__(kThreads) void tree_masks_kernel(const int32_t* __r
 // that ends within a group the next one goes on there, unless it would leave fewer than kLeast blocks on one side.
 // A group that is not cut may be written as it is, with a mark for the join (writes_whole); else every piece leaves its sums in the
 // workspace, and the last one of a group says so for the pieces that it does not have.  Where groups that are not cut are
-// written, a workgroup has two slots for the sums of the others: 512 slots of 256 rows, 64 MB for heads of 128, whatever
+// written, a workgroup has two slots for the sums of the others: 512 slots of 256 rows, 67 MB for heads of 128, whatever
 // the number of rows (with sums for every row and piece, 100 trees of 64 with 32 heads of 128 took 420 MB).  The lengths
 // are the device's, so each workgroup finds its part by going over the batch.
 //
@@ -213,7 +213,7 @@ int join_lanes(int D) { return D <= 64 ? 16 : D <= 128 ? 32 : 64; }
 
 // Whether groups that are not cut are written as they are.  The join then looks for their marks, which costs it a trip to
 // memory and some 1 us; many more rows than the chip holds at once are worth it: 204800 rows of 128, none cut, 51
-// us joined, 12 so; 52800 15.5 and 12; 29376, all cut, 13.3 and 14.8.
+// us joined, 11 so; 52800 15.5 and 11; 29376, all cut, 13.3 and 14.8.
 bool writes_whole(int64_t rows, int D) { return rows * join_lanes(D) > int64_t(4096) * 256; }
 
 // Joins the pieces of a row, LANES lanes to a row of up to 4 LANES values, always in the same order; most rows have few
