@@ -502,3 +502,39 @@ def test_cut_groups_leave_their_sums_in_slots(cr, B, Hq, H, D):
         heads = slice(0, Hq // H)                              # of the first cached head
         one = (cache[0][:, :1], cache[1][:, :1], cache[2][:, :1], cache[3][:, :1])
         check(outs[0][at, heads], q[at, heads], mask[at], cum([new[b]]), ln[b:b + 1], table[b:b + 1], one, 16, 1 / math.sqrt(D))
+
+
+def test_cut_groups_in_a_replayed_graph(cr):
+    """So many rows that whole groups are written, captured once; which groups are cut changes with the lengths on the
+    device from replay to replay, and on two streams at once."""
+    print("\n[case] tree attention, cut groups in a graph", flush=True)
+    gen = torch.Generator().manual_seed(52)
+    B, Hq, H, D, page, T = 12, 32, 2, 64, 32, 2400
+    table, pages = paging([4000] * B, page, gen)
+    cache = to(cache_of(pages, H, page, D, gen))
+    q = torch.randn((T, Hq, D), generator=gen).to(torch.bfloat16).to(DEV)
+    mask = random_mask(T, 4, gen).to(DEV)
+    table = table.to(DEV)
+    batches = []
+    for turn in range(4):
+        new = [int(torch.randint(0, 200, (1,), generator=gen)) for _ in range(B)]
+        lens = [n + int(torch.randint(0, (100, 3800, 900, 1)[turn], (1,), generator=gen)) for n in new]
+        batches.append((cum(new).to(DEV), i32(lens).to(DEV)))
+    cu, ln = (t.clone() for t in batches[0])
+    call = lambda c, l, **k: cr.convrot_kv8_tree_attention(q, mask, c, l, table, *cache, g=16, max_new=200, max_len=4000, **k)  # noqa: E731
+    out = torch.zeros((T, Hq, D), dtype=torch.bfloat16, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(cu, ln, out=out)
+    side = torch.cuda.Stream()
+    for turn in (0, 1, 2, 3, 1):
+        cu.copy_(batches[turn][0]), ln.copy_(batches[turn][1])
+        out.fill_(3)
+        side.wait_stream(torch.cuda.current_stream())
+        graph.replay()
+        with torch.cuda.stream(side):
+            want = call(*batches[turn], out=torch.full_like(out, 3.0))
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        rows = int(cu[-1])
+        assert bool((out[rows:] == 3).all()) and not bool((out[:rows] == 3).all())
